@@ -219,6 +219,18 @@ int mk_kv_set_pages(mk_ctx* ctx, int slot, const int32_t* pages_host, int n_page
 int mk_kv_get_pages(mk_ctx* ctx, int slot, int32_t* pages_out, int cap);
 int mk_kv_free_pages(mk_ctx* ctx);
 
+/* Beam search on KV-cache slots: positions [first, n_pos) of slot slots_host[b]
+ * become those of slot slots_host[parents_dev[b]], for all b in [0, n) at once
+ * and in place (slots_host NULL: slots 0..n-1; parents_dev: n int32 on the
+ * device, as mk_beam_select writes them; an entry outside [0, n) keeps its
+ * slot).  Slots whose parent is themselves are neither read nor written.  All
+ * parents 0 copies a prefilled prompt to every beam.  With a paged cache each
+ * slot gets the pages that n_pos positions need (MK_ERR_OOM when the pool has
+ * none).  MK_ERR_POS_RANGE unless 0 <= first <= n_pos <= max_seq.  Enqueued on the
+ * context's stream. */
+int mk_kv_reorder(mk_ctx* ctx, const int32_t* slots_host, int n, const int32_t* parents_dev,
+                  int first, int n_pos);
+
 /* n_steps greedy decode steps of request 0 in ONE persistent launch (the
  * device-resident loop): step s runs at position pos0 + s, feeds the id step
  * s - 1 produced (step 0 feeds token_dev[0]), appends its K/V and writes its
@@ -355,6 +367,148 @@ int mk_attention_decode(const float* q_dev, const void* k_dev, const void* v_dev
 int mk_attention_decode_noalloc(const float* q_dev, const void* k_dev, const void* v_dev,
                                 int n_keys, int n_q_per_kv, int head_dim, int splits,
                                 float* out_dev, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Operators on the state of a decode: a KV cache held in 4 bits with the
+ * attention over it and eviction by accumulated attention weight, and beam
+ * search's selection and reordering.  Like mk_attention_decode they need no
+ * context: they take device memory of the current device, enqueue on `stream`
+ * (which belongs to that device), allocate nothing, keep nothing from one call
+ * to the next and can be captured into a graph.  Argument errors return before
+ * anything is enqueued, with the reason in mk_last_error(NULL); sizes and
+ * indices that only the device sees (lengths, pages, parents) are checked
+ * there and cut or skipped as each operator says.  Results do not depend on
+ * timing: no operator uses atomics.  Calls that overlap on the GPU need
+ * workspaces of their own.
+ */
+#define MK_DTYPE_F32 0
+#define MK_DTYPE_BF16 1
+#define MK_DTYPE_F16 2
+
+/* A KV cache in 4 bits.  16 consecutive dims of a key or value row share an
+ * e4m3 scale, each dim is an e2m1 code (0 .5 1 1.5 2 3 4 6 and a sign): its
+ * value is code * scale * 2^k_log2 (keys) or 2^v_log2 (values), 4.5 bits.
+ * A block holds 32 keys of one KV head: K codes [32][d/2] (byte i: dim 2i in
+ * the low nibble, 2i+1 in the high), K scales [32][d/16], V codes, V scales; a
+ * page is [n_kv_heads][page_tokens/32] blocks, the pool [n_pages] pages of
+ * mk_kv4_page_bytes bytes.  Slot i of sequence s (its i-th key) is in page
+ * table[s][i / page_tokens]; a table entry outside [0, n_pages) is no page.
+ * lens_dev[s] counts the sequence's keys and belongs to the caller, who raises it
+ * before an append and lowers it after an eviction; one array serves
+ * the caches of all layers.  The device cuts it to [0, capacity], capacity =
+ * pages_per_seq * page_tokens.  scores_dev: the attention weight that each key
+ * has gathered.  Limits: head_dim 64 or 128, page_tokens a multiple of 32,
+ * n_seq <= 4096, n_kv_heads <= 1024, k_log2 and v_log2 in [-32, 32]; the pool 16-byte
+ * aligned. */
+typedef struct {
+  int n_kv_heads, head_dim, page_tokens, n_pages;
+  int n_seq, pages_per_seq;
+  int k_log2, v_log2;
+  void* pool_dev;
+  const int32_t* table_dev; /* [n_seq][pages_per_seq]; NULL: sequence s owns pages
+                               s * pages_per_seq .. of a pool of n_seq * pages_per_seq */
+  const int32_t* lens_dev;  /* [n_seq] */
+  float* scores_dev;        /* [n_seq][n_kv_heads][capacity], or NULL */
+} mk_kv4_cache;
+
+/* Bytes of one page; 0 for a shape that is not supported. */
+size_t mk_kv4_page_bytes(int n_kv_heads, int head_dim, int page_tokens);
+
+/* Appends packed tokens: tokens [offsets_dev[s], offsets_dev[s+1]) of k_dev and
+ * v_dev are the newest of sequence s and go to its slots
+ * lens[s] - count .. lens[s] - 1 (lens already counts them), their scores to 0.
+ * Rows are [n_kv_heads][head_dim] of `dtype` (MK_DTYPE_*), tokens k_stride and v_stride
+ * elements apart (so parts of a fused QKV row can be given); 16-byte aligned.
+ * Each group's scale is e4m3(max|x| / 6), to nearest even and at most 448;
+ * a code is the e2m1 value nearest to x / scale, halves to the even code, both
+ * decided exactly; |x| past 2688 * 2^log2 saturates, and a group that holds a
+ * NaN or an infinity reads back as NaN.  offsets_dev: n_seq + 1 int32, not
+ * decreasing; tokens outside them, slots outside the capacity and slots without a
+ * page are skipped.  Sequences must not share a page that is written. */
+int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const void* v_dev, int dtype,
+                  long long k_stride, long long v_stride, const int32_t* offsets_dev, int n_tokens,
+                  void* stream);
+
+/* Values of slots [0, min(n, lens[s])) of every sequence, to k_out_dev and
+ * v_out_dev [n_seq][n][n_kv_heads][head_dim] of `dtype` (bf16 holds them
+ * exactly, fp16 and fp32 as far as their range goes).  Rows of other slots,
+ * and of slots without a page, are left as they were. */
+int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, void* v_out_dev,
+                void* stream);
+
+/* Attention of the newest q_len tokens of every sequence over its cache, all
+ * query heads: token i of sequence s sees slots j < lens[s] - q_len + i + 1
+ * (its own key included), out = softmax(scale * q k^T) v.  q_dev: `dtype`
+ * [n_seq * q_len][n_q_heads][head_dim], tokens q_stride elements apart, 16-byte
+ * aligned; query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
+ * n_q_heads / n_kv_heads <= 1024.  out_dev: the same type,
+ * [n_seq][q_len][n_q_heads][head_dim].  fp32 softmax and sums; queries and
+ * probabilities enter the products with at least 22 bits (probabilities of a
+ * bf16 call 11).  A token that sees nothing gets zeros (a sequence shorter than
+ * q_len, an empty one); slots without a page are not seen, and what a masked
+ * slot holds never matters.  accumulate != 0 adds, for every slot, the weights
+ * of all tokens and query heads of its KV head to the cache's scores.
+ * workspace_dev: mk_attention_kv4_workspace_bytes(...) bytes (0: an argument
+ * is not supported), 16-byte aligned, any contents. */
+size_t mk_attention_kv4_workspace_bytes(const mk_kv4_cache* cache, int q_len, int n_q_heads,
+                                        int accumulate);
+int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, int dtype, int q_len,
+                     int n_q_heads, long long q_stride, float scale, int accumulate,
+                     void* workspace_dev, size_t workspace_bytes, void* out_dev, void* stream);
+
+/* Eviction by accumulated attention weight.  Of a sequence with more than
+ * `budget` keys every KV head keeps its first keep_first slots, its last
+ * keep_last and, between them, those with the highest scores (ties: the lowest
+ * slot; NaN lowest), budget in all; a shorter sequence keeps everything.  The
+ * kept rows go to slots 0, 1, ... of dst in slot order, bit for bit, with
+ * their scores; kept_dev [n_seq][n_kv_heads][budget] int32 receives the slots
+ * (-1 behind the last).  src is only read, so a prompt's pages may be shared;
+ * dst has pages and scores of its own (same heads, head_dim, n_seq and log2;
+ * page_tokens may differ), and its lens become min(lens, budget) by the
+ * caller.  1 <= budget <= dst's capacity; keep_first + keep_last <= budget. */
+int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, int budget, int keep_first,
+                 int keep_last, int32_t* kept_dev, void* stream);
+
+/* One step of beam search for n_batch searches of `beams` beams (1..16).  Row
+ * r = search * beams + beam of logits_dev (`dtype`, rows row_stride elements
+ * apart) gives candidates (beam, token) the score
+ * cum_dev[r] + log_softmax(logits)[token]; the `beams` highest of a search,
+ * compared in 64 bits, become its next beams, highest first (ties: the lowest
+ * beam, then the higher logit, then the lowest token).  A beam with
+ * finished_dev[r] != 0 has the one candidate (eos, cum) and its logits are not
+ * read.  -inf and NaN scores are no candidates; a search with fewer
+ * candidates than beams fills up with dead beams: score -inf, their own number as
+ * parent, token max(eos, 0).  Writes [n_batch][beams] tokens, parents (beam numbers inside
+ * the search), scores and, if asked, finished flags (the parent's, or token ==
+ * eos >= 0).  finished_dev (needs eos >= 0) and finished_out_dev may be NULL;
+ * outputs are arrays of their own.  vocab <= 1048576, n_batch * beams <= 65535.
+ * workspace_dev: mk_beam_select_workspace_bytes(...) bytes, 16-byte aligned,
+ * any contents. */
+size_t mk_beam_select_workspace_bytes(int n_batch, int beams, int vocab);
+int mk_beam_select(const void* logits_dev, int dtype, long long row_stride, const float* cum_dev,
+                   const uint8_t* finished_dev, int n_batch, int beams, int vocab, int eos,
+                   int32_t* tokens_dev, int32_t* parents_dev, float* scores_dev,
+                   uint8_t* finished_out_dev, void* workspace_dev, size_t workspace_bytes,
+                   void* stream);
+
+/* Reorders the beams' states in place: beam b of each search gets the state of
+ * beam parents_dev[search][b] (an entry outside [0, beams) keeps its own), all
+ * at once.  Row r = search * beams + b has n_segments segments of
+ * segment_bytes at state_dev + r * beam_stride + i * segment_stride -- say the
+ * generated positions of each layer and KV head; everything a multiple of 16
+ * bytes.  Beams that keep their state are neither read nor written. */
+int mk_beam_reorder(void* state_dev, const int32_t* parents_dev, int n_batch, int beams,
+                    size_t beam_stride, int n_segments, size_t segment_stride,
+                    size_t segment_bytes, void* stream);
+
+/* The same for a 4-bit cache whose sequences are searches of `beams` beams
+ * (n_seq a multiple of beams), through its table: the blocks that hold slots
+ * [first, n_keys), whole (first rounded down and n_keys up to a multiple of
+ * 32), and their scores (then 16-byte aligned).  Blocks that beams share
+ * physically stay as they are; any other block that moves belongs to one beam.
+ * Slots without a page are skipped. */
+int mk_kv4_reorder(const mk_kv4_cache* cache, const int32_t* parents_dev, int beams, int first,
+                   int n_keys, void* stream);
 
 /* Read-only HBM stream probe: every byte of src_dev[0, bytes) is loaded
  * once with 128-bit loads by a grid of (SMs x 4) CTAs; a value derived from

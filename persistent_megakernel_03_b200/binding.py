@@ -33,7 +33,10 @@ EXPORTS = ("mk_create", "mk_prefill", "mk_decode_step", "mk_decode_steps", "mk_d
            "mk_qkv_row_source", "mk_read_probe", "mk_set_trace", "mk_set_prefill_trace", "mk_inject_prefill_stall", "mk_prefill_graph",
            "mk_prefill_layout",
            "mk_attention_workspace_bytes", "mk_attention_decode",
-           "mk_attention_decode_noalloc", "mk_inject_stall")
+           "mk_attention_decode_noalloc", "mk_inject_stall", "mk_kv_reorder",
+           "mk_kv4_page_bytes", "mk_kv4_append", "mk_kv4_read", "mk_kv4_evict", "mk_kv4_reorder",
+           "mk_attention_kv4_workspace_bytes", "mk_attention_kv4", "mk_beam_select_workspace_bytes",
+           "mk_beam_select", "mk_beam_reorder")
 
 
 class MkError(RuntimeError):
@@ -69,6 +72,13 @@ class Options(C.Structure):
                 ("batch_sequential", C.c_int), ("prefill_steps", C.c_int),
                 ("kv_page_tokens", C.c_int), ("kv_pool_pages", C.c_int),
                 ("prefill_per_operator", C.c_int), ("prefill_attention", C.c_int)]
+
+
+class Kv4Struct(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("page_tokens", C.c_int),
+                ("n_pages", C.c_int), ("n_seq", C.c_int), ("pages_per_seq", C.c_int),
+                ("k_log2", C.c_int), ("v_log2", C.c_int), ("pool_dev", C.c_void_p),
+                ("table_dev", C.c_void_p), ("lens_dev", C.c_void_p), ("scores_dev", C.c_void_p)]
 
 
 class PlanInfo(C.Structure):
@@ -143,6 +153,21 @@ def lib(build_if_missing: bool = True):
     L.mk_attention_workspace_bytes.restype = C.c_size_t
     L.mk_attention_decode.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp]
     L.mk_attention_decode_noalloc.argtypes = [vp, vp, vp, i, i, i, i, vp, vp]
+    ll, sz, f = C.c_longlong, C.c_size_t, C.c_float
+    L.mk_kv_reorder.argtypes = [vp, ip, i, vp, i, i]
+    L.mk_kv4_page_bytes.argtypes = [i, i, i]
+    L.mk_kv4_page_bytes.restype = sz
+    L.mk_kv4_append.argtypes = [vp, vp, vp, i, ll, ll, vp, i, vp]
+    L.mk_kv4_read.argtypes = [vp, i, i, vp, vp, vp]
+    L.mk_kv4_evict.argtypes = [vp, vp, i, i, i, vp, vp]
+    L.mk_kv4_reorder.argtypes = [vp, vp, i, i, i, vp]
+    L.mk_attention_kv4_workspace_bytes.argtypes = [vp, i, i, i]
+    L.mk_attention_kv4_workspace_bytes.restype = sz
+    L.mk_attention_kv4.argtypes = [vp, vp, i, i, i, ll, f, i, vp, sz, vp, vp]
+    L.mk_beam_select_workspace_bytes.argtypes = [i, i, i]
+    L.mk_beam_select_workspace_bytes.restype = sz
+    L.mk_beam_select.argtypes = [vp, i, ll, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, sz, vp]
+    L.mk_beam_reorder.argtypes = [vp, vp, i, i, sz, i, sz, sz, vp]
     _lib = L
     return L
 
@@ -363,6 +388,57 @@ class Decoder:
         lib().mk_kv_get_pages(self.h, int(slot), out, n)
         return list(out)[:n]
 
+    def kv_reorder(self, parents_dev, first: int, n_pos: int, slots: Optional[Sequence[int]] = None):
+        """Positions [first, n_pos) of slot slots[b] (slot b without ``slots``)
+        become those of slot slots[parents_dev[b]], in place (see
+        mk_kv_reorder); ``parents_dev`` int32 CUDA, one entry per slot."""
+        import torch
+        _tensor(parents_dev, torch.int32, "parents_dev")
+        n = parents_dev.numel() if slots is None else len(slots)
+        if n != parents_dev.numel():
+            raise ValueError("one parent per slot")
+        _check(lib().mk_kv_reorder(self.h, None if slots is None else _ints(slots), n,
+                                   parents_dev.data_ptr(), int(first), int(n_pos)), self.h)
+
+    def beam_search(self, prompt_dev, beams: int, n_steps: int, eos: int = -1):
+        """The ``beams`` best continuations of a prompt (int32 CUDA) of at most
+        ``n_steps`` tokens, best first: (tokens [beams, n_steps] int32, sums of
+        log-probabilities [beams] fp32).  Sequences that reached ``eos`` (>= 0)
+        go on with it.  Uses slots 0..beams-1; after the prefill, steps,
+        selection and the caches' reordering are enqueued without a host round
+        trip."""
+        import torch
+        if not 1 <= beams <= self.max_batch:
+            raise ValueError("beams is 1 to max_batch")
+        n, V, dev = prompt_dev.numel(), self.model.vocab, prompt_dev.device
+        if n_steps < 1 or n + n_steps - 1 > self.max_seq:
+            raise ValueError("prompt and steps fit max_seq")
+        with torch.cuda.device(dev), torch.cuda.stream(self.stream):
+            logits = torch.empty(beams, V, device=dev)
+            cum, done = torch.full((2, 1, beams), float("-inf"), device=dev), None
+            cum[0, 0, 0] = 0.0                # one live beam: the prompt's
+            if eos >= 0:
+                done = torch.zeros(2, 1, beams, dtype=torch.bool, device=dev)
+            tok, par = torch.empty(2, 1, beams, dtype=torch.int32, device=dev)
+            ws = torch.empty(beam_select_workspace_bytes(1, beams, V), dtype=torch.uint8, device=dev)
+            seq = torch.empty(beams, n_steps, dtype=torch.int32, device=dev)
+            self.prefill_slots(prompt_dev, [0, n], [0], logits[:1])
+            logits[1:] = logits[:1]           # not read for candidates: their sums are -inf
+            self.kv_reorder(torch.zeros(beams, dtype=torch.int32, device=dev), 0, n)
+            for s in range(n_steps):
+                a, b = s % 2, (s + 1) % 2
+                beam_select(logits, cum[a], tok, par, cum[b], ws,
+                            finished=None if done is None else done[a],
+                            finished_out=None if done is None else done[b], eos=eos,
+                            stream=self.stream)
+                if s:
+                    self.kv_reorder(par.view(-1), n, n + s)
+                    seq[:, :s] = seq[:, :s][par.view(-1).long()]
+                seq[:, s] = tok.view(-1)
+                if s + 1 < n_steps:
+                    self.decode_slots(tok.view(-1), [n + s] * beams, list(range(beams)), logits)
+        return seq, cum[n_steps % 2].view(-1)
+
     def kv_free_pages(self) -> int:
         n = lib().mk_kv_free_pages(self.h)
         _check(min(n, 0), self.h)
@@ -457,3 +533,215 @@ def attention_decode_noalloc(q_dev, k_dev, v_dev, n_keys: int, splits: int, out_
     _check(lib().mk_attention_decode_noalloc(q_dev.data_ptr(), k_dev.data_ptr(),
                                              v_dev.data_ptr(), int(n_keys), int(G), int(d),
                                              int(splits), out_dev.data_ptr(), st.cuda_stream))
+
+
+# ------------------------------------- the state of a decode: 4-bit cache, beams
+
+def _dtype(t) -> int:
+    import torch
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"fp32, bf16 or fp16 expected, got {t.dtype}")
+    return code
+
+
+def _tensor(t, dtype, what, shape=None):
+    if not t.is_cuda or (dtype is not None and t.dtype != dtype) or not t.is_contiguous():
+        raise TypeError(f"{what}: a contiguous CUDA tensor{'' if dtype is None else f' of {dtype}'} expected")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on(device, stream, call, *args):
+    """Runs ``call(*args, stream)`` on the tensors' device; the stream is
+    ``stream``, or that device's current one."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        _check(call(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, stream.cuda_stream))
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors on one device: {t.device} and {device}")
+
+
+def kv4_page_bytes(n_kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    return int(lib().mk_kv4_page_bytes(n_kv_heads, head_dim, page_tokens))
+
+
+class Kv4Cache:
+    """A 4-bit KV cache in the caller's tensors (see mk_kv4_cache): ``pool``
+    uint8 [pages, kv4_page_bytes(...)], ``lens`` int32 [n_seq], ``table`` int32
+    [n_seq, pages_per_seq] (None: sequence s owns the s-th run of pages),
+    ``scores`` fp32 [n_seq, n_kv_heads, pages_per_seq * page_tokens] or None.
+    Holds the tensors, copies nothing; their contents may change between
+    calls, their storage not."""
+
+    def __init__(self, pool, lens, n_kv_heads: int, head_dim: int, page_tokens: int, table=None,
+                 scores=None, k_log2: int = 0, v_log2: int = 0):
+        import torch
+        L = lib()
+        page = L.mk_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
+        if page == 0:
+            raise MkError(-9, "head_dim is 64 or 128, page_tokens a multiple of 32")
+        if pool.dim() != 2 or lens.dim() != 1 or pool.shape[1] != page:
+            raise ValueError(f"pool is [pages, {page}], lens [n_seq]")
+        self.n_seq = lens.shape[0]
+        if table is None:
+            if self.n_seq == 0 or pool.shape[0] % self.n_seq:
+                raise ValueError("without a table every sequence has the same number of pages")
+            per = pool.shape[0] // self.n_seq
+        else:
+            if table.dim() != 2 or table.shape[0] != self.n_seq:
+                raise ValueError("table is [n_seq, pages_per_seq]")
+            per = table.shape[1]
+        self.capacity = per * page_tokens
+        self.n_kv_heads, self.head_dim, self.page_tokens = n_kv_heads, head_dim, page_tokens
+        self.pool, self.lens, self.table, self.scores = pool, lens, table, scores
+        self.device = pool.device
+        _same_device(self.device, lens, table, scores)
+        self.c = Kv4Struct(n_kv_heads, head_dim, page_tokens, pool.shape[0], self.n_seq, per, k_log2,
+                           v_log2, _tensor(pool, torch.uint8, "pool"),
+                           None if table is None else _tensor(table, torch.int32, "table"),
+                           _tensor(lens, torch.int32, "lens"),
+                           None if scores is None else _tensor(
+                               scores, torch.float32, "scores", (self.n_seq, n_kv_heads, self.capacity)))
+        self.ref = C.addressof(self.c)
+
+
+def _rows(t, heads, dim, what):
+    """(pointer, elements between tokens) of token rows [..., heads, dim] whose
+    heads lie together."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what}: CUDA [tokens, {heads}, {dim}] expected, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{what}: a token's heads and dims are contiguous")
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * dim
+
+
+def kv4_append(cache: Kv4Cache, k, v, offsets, stream=None):
+    """Packed new tokens k, v [tokens, n_kv_heads, head_dim] (token rows may be
+    strided) into the cache; tokens offsets[s]..offsets[s+1] are the newest of
+    sequence s, which cache.lens counts already (see mk_kv4_append)."""
+    import torch
+    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
+    if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
+        raise ValueError("k and v have the same tokens and type")
+    _same_device(cache.device, k, v, offsets)
+    _on(cache.device, stream, lib().mk_kv4_append, cache.ref, kp, vp, _dtype(k), ks, vs,
+        _tensor(offsets, torch.int32, "offsets", (cache.n_seq + 1,)), k.shape[0])
+
+
+def kv4_read(cache: Kv4Cache, k_out, v_out, stream=None):
+    """Values of slots [0, min(n, lens)) into k_out, v_out [n_seq, n,
+    n_kv_heads, head_dim]; other rows are left (see mk_kv4_read)."""
+    n = k_out.shape[1]
+    shape = (cache.n_seq, n, cache.n_kv_heads, cache.head_dim)
+    _same_device(cache.device, k_out, v_out)
+    _on(cache.device, stream, lib().mk_kv4_read, cache.ref, _dtype(k_out), n,
+        _tensor(k_out, None, "k_out", shape), _tensor(v_out, k_out.dtype, "v_out", shape))
+
+
+def attention_kv4_workspace_bytes(cache: Kv4Cache, q_len: int, n_q_heads: int,
+                                  accumulate: bool = False) -> int:
+    return int(lib().mk_attention_kv4_workspace_bytes(cache.ref, q_len, n_q_heads, int(accumulate)))
+
+
+def attention_kv4(cache: Kv4Cache, q, out, workspace, scale: Optional[float] = None,
+                  accumulate: bool = False, stream=None):
+    """Attention of the newest q_len tokens of every sequence, q and out
+    [n_seq, q_len, n_q_heads, head_dim], over the cache; ``scale`` is
+    1/sqrt(head_dim) unless given, ``accumulate`` adds the weights to
+    cache.scores (see mk_attention_kv4)."""
+    if q.dim() != 4 or q.shape[0] != cache.n_seq or q.shape[3] != cache.head_dim:
+        raise ValueError(f"q: [{cache.n_seq}, q_len, n_q_heads, {cache.head_dim}] expected, got {tuple(q.shape)}")
+    n_seq, q_len, heads, dim = q.shape
+    st = q.stride()
+    row = st[1] if q_len > 1 else (st[0] if n_seq > 1 else heads * dim)
+    if not q.is_cuda or st[3] != 1 or (heads > 1 and st[2] != dim) or (n_seq > 1 and st[0] != q_len * row):
+        raise ValueError("q: a token's heads and dims are contiguous, tokens evenly spaced")
+    _same_device(cache.device, q, out, workspace)
+    _on(cache.device, stream, lib().mk_attention_kv4, cache.ref, q.data_ptr(), _dtype(q), q_len, heads, row,
+        dim ** -0.5 if scale is None else scale, int(accumulate), _tensor(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _tensor(out, q.dtype, "out", q.shape))
+
+
+def kv4_evict(src: Kv4Cache, dst: Kv4Cache, budget: int, keep_first: int, keep_last: int, kept,
+              stream=None):
+    """The rows of src that a budget leaves -- its ends and the highest scores
+    -- into dst, their slots into kept int32 [n_seq, n_kv_heads, budget] (see
+    mk_kv4_evict)."""
+    import torch
+    _same_device(src.device, dst.pool, kept)
+    _on(src.device, stream, lib().mk_kv4_evict, src.ref, dst.ref, budget, keep_first, keep_last,
+        _tensor(kept, torch.int32, "kept", (src.n_seq, src.n_kv_heads, budget)))
+
+
+def kv4_reorder(cache: Kv4Cache, parents, first: int, n_keys: int, stream=None):
+    """Reorders the sequences of each search in place: parents int32
+    [n_seq / beams, beams] (see mk_kv4_reorder)."""
+    import torch
+    if parents.dim() != 2 or parents.numel() != cache.n_seq:
+        raise ValueError("parents is [searches, beams], one entry per sequence")
+    _same_device(cache.device, parents)
+    _on(cache.device, stream, lib().mk_kv4_reorder, cache.ref, _tensor(parents, torch.int32, "parents"),
+        parents.shape[1], first, n_keys)
+
+
+def beam_select_workspace_bytes(n_batch: int, beams: int, vocab: int) -> int:
+    return int(lib().mk_beam_select_workspace_bytes(n_batch, beams, vocab))
+
+
+def beam_select(logits, cum, tokens, parents, scores, workspace, finished=None, finished_out=None,
+                eos: int = -1, stream=None):
+    """The next beams of every search: logits [n_batch * beams, vocab] (rows may
+    be strided), cum fp32 [n_batch, beams] -> tokens, parents int32, scores
+    fp32 and finished_out (bool or uint8), all [n_batch, beams] (see
+    mk_beam_select)."""
+    import torch
+    shape = cum.shape
+    if len(shape) != 2 or logits.dim() != 2 or logits.shape[0] != shape[0] * shape[1]:
+        raise ValueError("cum is [n_batch, beams], logits [n_batch * beams, vocab]")
+    if not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: CUDA, contiguous rows")
+    for f in (finished, finished_out):
+        if f is not None and f.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("finished flags are bool or uint8")
+    _same_device(logits.device, cum, tokens, parents, scores, workspace, finished, finished_out)
+    _on(logits.device, stream, lib().mk_beam_select, logits.data_ptr(), _dtype(logits),
+        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], _tensor(cum, torch.float32, "cum"),
+        None if finished is None else _tensor(finished, None, "finished", shape), shape[0], shape[1],
+        logits.shape[1], eos, _tensor(tokens, torch.int32, "tokens", shape),
+        _tensor(parents, torch.int32, "parents", shape), _tensor(scores, torch.float32, "scores", shape),
+        None if finished_out is None else _tensor(finished_out, None, "finished_out", shape),
+        _tensor(workspace, None, "workspace"), workspace.numel() * workspace.element_size())
+
+
+def beam_reorder(state, parents, first: int, count: int, stream=None):
+    """Reorders states [n_batch * beams, segments, positions, ...] (contiguous,
+    any type) in place by parents int32 [n_batch, beams]; positions [first,
+    first + count) of every segment move, the others stay (see
+    mk_beam_reorder)."""
+    import torch
+    base = _tensor(state, None, "state")
+    if state.dim() < 3 or parents.dim() != 2 or parents.numel() != state.shape[0]:
+        raise ValueError("state is [n_batch * beams, segments, positions, ...], parents [n_batch, beams]")
+    segments, positions = state.shape[1], state.shape[2]
+    if first < 0 or count < 0 or first + count > positions:
+        raise ValueError("positions [first, first + count) of the state")
+    if state.numel() == 0 or count == 0:
+        return
+    row = state.element_size() * state.stride(2)
+    _same_device(state.device, parents)
+    _on(state.device, stream, lib().mk_beam_reorder, base + first * row,
+        _tensor(parents, torch.int32, "parents"), parents.shape[0], parents.shape[1],
+        segments * positions * row, segments, positions * row, count * row)

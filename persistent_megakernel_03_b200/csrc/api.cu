@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "../../include/mk.h"
+#include "beam.h"
 #include "mk_internal.h"
 #include "plan.h"
 #include "prefill.h"
@@ -838,6 +839,48 @@ extern "C" int mk_kv_release(mk_ctx* ctx, int slot) {
     ctx->kv_pending.emplace_back(slot * ctx->kv_pps + i, -1);
   }
   return kv_flush(ctx);
+}
+
+// Beam search's states (beam.cu moves them): the positions of both caches, in
+// their pages.
+extern "C" int mk_kv_reorder(mk_ctx* ctx, const int32_t* slots_host, int n, const int32_t* parents_dev,
+                             int first, int n_pos) {
+  int rc = check_ctx(ctx);
+  if (rc) return rc;
+  const mk_config& c = ctx->cfg;
+  if (n < 1 || n > c.max_batch) return fail(ctx, MK_ERR_INVALID_ARG, "the number of slots is 1 to max_batch");
+  if (!parents_dev || (reinterpret_cast<uintptr_t>(parents_dev) & 3u))
+    return fail(ctx, MK_ERR_INVALID_ARG, "parents are a 4-byte aligned device array");
+  if (first < 0 || n_pos < first || n_pos > c.max_seq)
+    return fail(ctx, MK_ERR_POS_RANGE, "positions [first, n_pos) lie in [0, max_seq]");
+  int32_t slots[kMaxBatch];
+  if ((rc = resolve_slots(ctx, slots_host, n, slots))) return rc;
+  if (n_pos == first) return MK_OK;
+  for (int i = 0; i < n; ++i)
+    if ((rc = kv_ensure(ctx, slots[i], n_pos))) { kv_flush(ctx); return rc; }
+  if ((rc = kv_flush(ctx))) return rc;
+  ReorderArgs a = {};
+  a.parents = parents_dev;
+  a.beams = n;
+  a.n_states = 2;
+  const uint32_t row16 = (uint32_t)c.head_dim * 2 / 16;
+  for (int i = 0; i < 2; ++i) {
+    ReorderState& s = a.state[i];
+    s.base = reinterpret_cast<uint8_t*>(i ? ctx->md.vcache : ctx->md.kcache);
+    s.table = ctx->kv_table_d;
+    s.pps = ctx->kv_pps;
+    s.pages = ctx->kv_pool;
+    s.page16 = (uint32_t)ctx->kv_page * row16;
+    s.seg_stride = (size_t)s.page16 * 16;
+    s.segments = c.n_layers * c.n_kv_heads;
+    s.stride = s.seg_stride * s.segments;
+    s.first16 = (uint32_t)first * row16;
+    s.count16 = (uint32_t)(n_pos - first) * row16;
+    s.slots = 1;
+    for (int b = 0; b < n; ++b) s.slot[b] = slots[b];
+  }
+  CK(launch_reorder(a, 1, ctx->stream));
+  return MK_OK;
 }
 
 extern "C" int mk_kv_set_pages(mk_ctx* ctx, int slot, const int32_t* pages_host, int n_pages) {

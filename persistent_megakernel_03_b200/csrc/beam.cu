@@ -1,0 +1,527 @@
+// beam.cu -- beam search: the selection over beams and vocabulary, and the
+// reordering of the beams' states.
+#include <math.h>
+#include <stdio.h>
+
+#include "kv4.cuh"
+#include "pdl.cuh"
+#include "beam.h"
+
+namespace mk {
+namespace {
+
+// ------------------------------------------------------------------ select
+//
+// Candidate (b, v) of a search has the score cum[b] + logit[b][v] - lse(logit[b]);
+// the W highest are wanted.  Inside a beam the order is that of the logits, so
+// no score is needed to find a beam's own W best: the vocabulary is read once,
+// in chunks of 4,096 that stay in registers, and each chunk gives its W
+// highest logits, its maximum and its sum of exponentials.  A second kernel,
+// one CTA a search and one warp a beam, joins the chunks: the log-sum-exp, the
+// beam's W best (they lie in the W chunks with the highest heads), then the
+// best of W * W scores.  Scores are compared in 64 bits, so that candidates of
+// different beams are not ordered by rounding.
+//
+// Bound: the logits' bytes once (4.1 MB for 8 beams of 128,256 in fp32: under
+// 1 us) beside two launches and W rounds of warp maxima in each.
+
+constexpr int kThreadsS = 256;
+constexpr int kWarpsS = kThreadsS / 32;
+constexpr int kPer = 16;                        // logits of a thread
+constexpr int kChunk = kThreadsS * kPer;
+constexpr int kMaxBeams = 16;
+constexpr int kMaxChunks = 256;                 // vocabulary up to 1,048,576
+constexpr int kHeads = kMaxChunks / 32;         // chunk heads of a lane
+
+// fp32 to an integer of the same order; 0 for what is no candidate (-inf, NaN).
+__device__ __forceinline__ uint32_t logit_key(float f) {
+  if (!(f > -INFINITY)) return 0u;
+  if (f == 0.f) return 0x80000000u;
+  const uint32_t b = __float_as_uint(f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// The lane whose (key, index) is first: highest key, then lowest index.
+__device__ __forceinline__ void warp_first(uint32_t key, uint32_t idx, uint32_t& k, uint32_t& i) {
+  k = __reduce_max_sync(0xFFFFFFFFu, key);
+  i = __reduce_min_sync(0xFFFFFFFFu, key == k ? idx : 0xFFFFFFFFu);
+}
+
+struct SelectArgs {
+  const void* logits;
+  size_t stride;              // bytes between rows
+  const float* cum;
+  const uint8_t* finished;    // null: none
+  int32_t* tokens;
+  int32_t* parents;
+  float* scores;
+  uint8_t* done;              // null: not wanted
+  int32_t dtype, beams, vocab, chunks, eos, wide;   // wide: 16-byte loads
+  // workspace
+  float2* sums;               // [rows][chunks]: maximum, sum of exp(x - maximum)
+  uint2* lists;               // [rows][chunks][beams]: key, token, highest first
+};
+
+__global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs a) {
+  __shared__ uint2 best[kWarpsS][kMaxBeams];
+  __shared__ uint32_t tops[kWarpsS];
+  __shared__ float parts[kWarpsS];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = a.beams;
+  const size_t row = blockIdx.y;
+  if (a.finished && __ldcg(a.finished + row)) return;   // has its one candidate
+  const int c0 = blockIdx.x * kChunk;
+  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.stride;
+  float x[kPer];
+  // wide: element e of load j is c0 + (j * threads + tid) * per + e, per = 4 or 8
+  const int per = a.wide ? (a.dtype == MK_DTYPE_F32 ? 4 : 8) : 1;
+  auto at = [&](int i) { return c0 + ((i / per) * kThreadsS + (int)threadIdx.x) * per + i % per; };
+  if (a.dtype == MK_DTYPE_F32) {
+    const float* p = reinterpret_cast<const float*>(base);
+    if (a.wide) {
+#pragma unroll
+      for (int j = 0; j < kPer / 4; ++j) {
+        const int i = c0 + (j * kThreadsS + threadIdx.x) * 4;
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (i + 3 < a.vocab) v = __ldcg(reinterpret_cast<const float4*>(p + i));
+        else {
+          if (i < a.vocab) v.x = __ldcg(p + i);
+          if (i + 1 < a.vocab) v.y = __ldcg(p + i + 1);
+          if (i + 2 < a.vocab) v.z = __ldcg(p + i + 2);
+        }
+        x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = c0 + j * kThreadsS + threadIdx.x;
+        x[j] = i < a.vocab ? __ldcg(p + i) : -INFINITY;
+      }
+    }
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(base);
+    const bool bf = a.dtype == MK_DTYPE_BF16;
+    auto widen = [&](uint32_t h) {
+      return bf ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+    };
+    if (a.wide) {
+#pragma unroll
+      for (int j = 0; j < kPer / 8; ++j) {
+        const int i = c0 + (j * kThreadsS + threadIdx.x) * 8;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const bool whole = i + 7 < a.vocab;
+        if (whole) v = __ldcg(reinterpret_cast<const uint4*>(p + i));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (whole) x[8 * j + e] = widen(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
+          else x[8 * j + e] = i + e < a.vocab ? widen(__ldcg(p + i + e)) : -INFINITY;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = c0 + j * kThreadsS + threadIdx.x;
+        x[j] = i < a.vocab ? widen(__ldcg(p + i)) : -INFINITY;
+      }
+    }
+  }
+
+  uint32_t key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = logit_key(x[i]);
+  uint32_t mine = 0, which = 0;   // this lane's first: the lowest index of its highest key
+  auto rescan = [&]() {
+    mine = 0; which = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] > mine) { mine = key[i]; which = i; }   // at() grows with i
+  };
+  rescan();
+  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, mine);
+  if (lane == 0) tops[warp] = top;
+  // this warp's W highest
+  for (int j = 0; j < W; ++j) {
+    uint32_t k, i;
+    warp_first(mine, at(which), k, i);
+    if (lane == 0) best[warp][j] = make_uint2(k, i);
+    if (k == 0u) {   // no more candidates
+      for (int z = j + 1 + lane; z < W; z += 32) best[warp][z] = make_uint2(0u, 0u);
+      break;
+    }
+    if (mine == k && (uint32_t)at(which) == i) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (e == (int)which) key[e] = 0u;
+      rescan();
+    }
+  }
+  __syncthreads();
+  uint32_t m = 0;
+#pragma unroll
+  for (int w = 0; w < kWarpsS; ++w) m = max(m, tops[w]);
+  const float mx = m ? key_logit(m) : 0.f;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sum += exp2f((x[i] - mx) * 1.44269504f);   // -inf adds 0, NaN goes through
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) parts[warp] = sum;
+  __syncthreads();
+  if (warp) return;
+  const size_t chunk = row * a.chunks + blockIdx.x;
+  if (lane == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarpsS; ++w) s += parts[w];
+    a.sums[chunk] = make_float2(m ? mx : -INFINITY, s);
+  }
+  // join of the warps' lists: lane l (of kWarpsS) walks list l
+  uint2* out = a.lists + chunk * W;
+  int head = 0;
+  uint2 h = lane < kWarpsS ? best[lane][0] : make_uint2(0u, 0u);
+  for (int j = 0; j < W; ++j) {
+    uint32_t k, i;
+    warp_first(h.x, h.y, k, i);
+    if (lane == 0) out[j] = make_uint2(k, k ? i : 0u);
+    if (k && h.x == k && h.y == i) {
+      ++head;
+      h = head < W ? best[lane][head] : make_uint2(0u, 0u);
+    }
+  }
+}
+
+// 64-bit scores to integers of the same order; 0 for what is no candidate.
+__device__ __forceinline__ unsigned long long score_key64(double s) {
+  if (!(s > -INFINITY)) return 0ull;
+  if (s == 0.0) return 0x8000000000000000ull;
+  const unsigned long long b = __double_as_longlong(s);
+  return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+
+constexpr int kFinal = kMaxBeams * kMaxBeams / 32;   // candidates of a lane
+
+__global__ void __launch_bounds__(kMaxBeams * 32) beam_join_kernel(const SelectArgs a) {
+  __shared__ unsigned long long cand_key[kMaxBeams * kMaxBeams];
+  __shared__ double cand_score[kMaxBeams * kMaxBeams];
+  __shared__ int32_t cand_token[kMaxBeams * kMaxBeams];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5, W = a.beams;
+  const size_t row = (size_t)blockIdx.x * W + beam;
+  const double cum = __ldcg(a.cum + row);
+  const bool finished = a.finished && __ldcg(a.finished + row);
+  if (finished) {
+    for (int j = lane; j < W; j += 32) {
+      const bool one = j == 0;
+      cand_key[beam * W + j] = one ? score_key64(cum) : 0ull;
+      cand_score[beam * W + j] = cum;
+      cand_token[beam * W + j] = a.eos;
+    }
+  } else {
+    // log-sum-exp over the chunks
+    const float2* sums = a.sums + row * a.chunks;
+    float mx = -INFINITY;
+    for (int c = lane; c < a.chunks; c += 32) mx = fmaxf(mx, __ldcg(sums + c).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    double sum = 0.0;
+    for (int c = lane; c < a.chunks; c += 32) {
+      const float2 s = __ldcg(sums + c);
+      // a chunk without a candidate has maximum -inf and adds its sum: 0, or a NaN
+      sum += s.x > -INFINITY ? (double)s.y * exp((double)s.x - (double)mx) : (double)s.y;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const double lse = (double)mx + log(sum);
+    // the W chunks with the highest heads
+    const uint2* lists = a.lists + row * a.chunks * W;
+    uint2 head[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int c = i * 32 + lane;
+      head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
+    }
+    int chosen = -1;   // lane j: the j-th of them
+    for (int j = 0; j < W; ++j) {
+      uint32_t mine = 0, tok = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (head[i].x > mine) { mine = head[i].x; tok = head[i].y; }   // chunks grow with i
+      uint32_t k, t;
+      warp_first(mine, tok, k, t);
+      if (k == 0u) break;
+      if (lane == j) chosen = (int)t / kChunk;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (head[i].x == k && head[i].y == t) head[i].x = 0u;
+    }
+    // their lists: W * W keys, a lane's share in registers
+    uint2 c[kFinal];
+#pragma unroll
+    for (int i = 0; i < kFinal; ++i) {
+      const int e = i * 32 + lane, from = e / W;
+      const int chunk = __shfl_sync(0xFFFFFFFFu, chosen, from & 31);
+      c[i] = e < W * W && chunk >= 0 ? __ldcg(lists + (size_t)chunk * W + (e - from * W)) : make_uint2(0u, 0u);
+    }
+    for (int j = 0; j < W; ++j) {
+      uint32_t mine = 0, tok = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < kFinal; ++i)
+        if (c[i].x > mine || (c[i].x == mine && mine && c[i].y < tok)) { mine = c[i].x; tok = c[i].y; }
+      uint32_t k, t;
+      warp_first(mine, tok, k, t);
+#pragma unroll
+      for (int i = 0; i < kFinal; ++i)
+        if (c[i].x == k && c[i].y == t) c[i].x = 0u;
+      if (lane == 0) {
+        const double s = k ? cum + ((double)key_logit(k) - lse) : -INFINITY;
+        cand_key[beam * W + j] = score_key64(s);
+        cand_score[beam * W + j] = s;
+        cand_token[beam * W + j] = (int32_t)t;
+      }
+    }
+  }
+  __syncthreads();
+  if (beam) return;
+  // the W first of W * W: highest score, then lowest beam, then the beam's own order
+  unsigned long long key[kFinal];
+#pragma unroll
+  for (int i = 0; i < kFinal; ++i) key[i] = i * 32 + lane < W * W ? cand_key[i * 32 + lane] : 0ull;
+  for (int j = 0; j < W; ++j) {
+    unsigned long long mine = 0;
+    uint32_t idx = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kFinal; ++i)
+      if (key[i] > mine) { mine = key[i]; idx = i * 32 + lane; }
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(mine >> 32));
+    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+    const unsigned long long k = (unsigned long long)hi << 32 | lo;
+    const uint32_t who = __reduce_min_sync(0xFFFFFFFFu, mine == k ? idx : 0xFFFFFFFFu);
+#pragma unroll
+    for (int i = 0; i < kFinal; ++i)
+      if (i * 32 + lane == (int)who) key[i] = 0ull;
+    if (lane == 0) {
+      const size_t to = (size_t)blockIdx.x * W + j;
+      // fewer candidates than beams: a dead one, which keeps its own state
+      const int parent = k ? (int)who / W : j, token = k ? cand_token[who] : max(a.eos, 0);
+      a.tokens[to] = token;
+      a.parents[to] = parent;
+      a.scores[to] = k ? (float)cand_score[who] : -INFINITY;
+      if (a.done)
+        a.done[to] = (a.finished && __ldcg(a.finished + (size_t)blockIdx.x * W + parent)) ||
+                     (a.eos >= 0 && token == a.eos);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- reorder
+//
+// Beam b gets the state of beam parents[b], in place.  A thread owns one
+// 16-byte column of the states: it reads that column of every parent that some
+// other beam wants, and only then writes, so no beam's state is overwritten
+// before it is read and no copy of the states is kept.  Beams that stay are neither
+// read nor written.  Bound: the moved bytes, read (once from HBM per parent) and written.
+
+constexpr int kThreadsR = 256;
+
+// Physical byte address of logical offset `o` (in the beam's segment `seg`).
+__device__ __forceinline__ uint8_t* state_at(const ReorderState& s, int beam, int seg, uint32_t o16) {
+  int slot = s.slots ? s.slot[beam] : beam;
+  uint32_t page = (uint32_t)slot;
+  if (s.page16) {   // pages of a segment: page16 16-byte columns each
+    const uint32_t lp = o16 / s.page16;
+    o16 -= lp * s.page16;
+    if (s.table) {
+      const int p = __ldcg(s.table + (size_t)slot * s.pps + lp);
+      if (p < 0 || p >= s.pages) return nullptr;
+      page = (uint32_t)p;
+    } else {
+      page = (uint32_t)slot * s.pps + lp;
+    }
+  }
+  return s.base + page * s.stride + seg * s.seg_stride + (size_t)o16 * 16;
+}
+
+template <int W>
+__global__ void __launch_bounds__(kThreadsR) beam_reorder_kernel(const ReorderArgs a) {
+  __shared__ int par[W];
+  pdl_trigger();
+  pdl_wait();
+  const ReorderState& s = a.state[blockIdx.z % a.n_states];
+  const int batch = blockIdx.z / a.n_states;
+  if (threadIdx.y == 0 && threadIdx.x < W) {
+    const int b = threadIdx.x;
+    int p = b < a.beams ? __ldcg(a.parents + (size_t)batch * a.beams + b) : b;
+    par[b] = p < 0 || p >= a.beams ? b : p;   // no such beam: it stays
+  }
+  __syncthreads();
+  const int seg = blockIdx.y * blockDim.y + threadIdx.y;
+  const uint32_t col = blockIdx.x * blockDim.x + threadIdx.x;
+  if (seg >= s.segments || col >= s.count16) return;
+  const uint32_t o = s.first16 + col;
+  uint4 v[W];
+  uint32_t moves = 0;
+#pragma unroll
+  for (int b = 0; b < W; ++b) {
+    const int p = par[b];
+    if (b < a.beams && p != b) {
+      const uint8_t* from = state_at(s, batch * a.beams + p, seg, o);
+      if (from) { v[b] = __ldcg(reinterpret_cast<const uint4*>(from)); moves |= 1u << b; }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < W; ++b)
+    if (moves >> b & 1u) {
+      uint8_t* to = state_at(s, batch * a.beams + b, seg, o);
+      if (to) *reinterpret_cast<uint4*>(to) = v[b];
+    }
+}
+
+int fail(int code, const char* who, const char* why) { return kv4_fail(code, who, why); }
+
+}  // namespace
+
+cudaError_t launch_reorder(const ReorderArgs& a, int n_batch, cudaStream_t st) {
+  uint32_t cols = 0;
+  int segs = 0;
+  for (int i = 0; i < a.n_states; ++i) {
+    if (a.state[i].count16 > cols) cols = a.state[i].count16;
+    if (a.state[i].segments > segs) segs = a.state[i].segments;
+  }
+  if (cols == 0 || segs == 0 || a.beams < 2) return cudaSuccess;
+  int x = 32;   // short segments share a block
+  while (x < kThreadsR && (uint32_t)x < cols) x <<= 1;
+  const int y = kThreadsR / x;
+  const dim3 grid((cols + x - 1) / x, (segs + y - 1) / y, n_batch * a.n_states), block(x, y);
+  if (grid.y > 65535u || grid.z > 65535u) return cudaErrorInvalidValue;
+  auto kernel = a.beams <= 2 ? beam_reorder_kernel<2> : a.beams <= 4 ? beam_reorder_kernel<4>
+                : a.beams <= 8 ? beam_reorder_kernel<8> : beam_reorder_kernel<16>;
+  return pdl_launch(kernel, grid, block, 0, st, a);
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" size_t mk_beam_select_workspace_bytes(int n_batch, int beams, int vocab) {
+  if (n_batch < 1 || beams < 1 || beams > kMaxBeams || vocab < 1 || vocab > kChunk * kMaxChunks ||
+      (long long)n_batch * beams > 65535)
+    return 0;
+  const size_t chunks = (vocab + kChunk - 1) / kChunk, rows = (size_t)n_batch * beams;
+  return rows * chunks * (sizeof(float2) + beams * sizeof(uint2));
+}
+
+extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_stride, const float* cum_dev,
+                              const uint8_t* finished_dev, int n_batch, int beams, int vocab, int eos,
+                              int32_t* tokens_dev, int32_t* parents_dev, float* scores_dev,
+                              uint8_t* finished_out_dev, void* workspace_dev, size_t workspace_bytes,
+                              void* stream) {
+  const char* who = "mk_beam_select";
+  if (n_batch < 1 || beams < 1 || beams > kMaxBeams || (long long)n_batch * beams > 65535)
+    return fail(MK_ERR_INVALID_ARG, who, "1 to 16 beams, and at most 65535 rows");
+  if (vocab < 1 || vocab > kChunk * kMaxChunks) return fail(MK_ERR_INVALID_ARG, who, "vocab is 1 to 1048576");
+  const int esz = dtype == MK_DTYPE_F32 ? 4 : (dtype == MK_DTYPE_BF16 || dtype == MK_DTYPE_F16) ? 2 : 0;
+  if (!esz) return fail(MK_ERR_INVALID_ARG, who, "dtype is one of MK_DTYPE_*");
+  if (!logits_dev || !cum_dev || !tokens_dev || !parents_dev || !scores_dev)
+    return fail(MK_ERR_INVALID_ARG, who, "logits, sums, tokens, parents and scores are wanted");
+  if (row_stride < vocab || row_stride > (1ll << 40)) return fail(MK_ERR_INVALID_ARG, who, "rows are at least vocab apart");
+  if (eos < -1 || eos >= vocab) return fail(MK_ERR_INVALID_ARG, who, "eos is -1 or a token");
+  if (finished_dev && eos < 0) return fail(MK_ERR_INVALID_ARG, who, "finished beams need an eos");
+  if (finished_dev && (const uint8_t*)finished_out_dev == finished_dev)
+    return fail(MK_ERR_INVALID_ARG, who, "finished flags are read while the new ones are written: two arrays");
+  if (static_cast<const float*>(scores_dev) == cum_dev)
+    return fail(MK_ERR_INVALID_ARG, who, "sums are read while the new ones are written: two arrays");
+  if ((reinterpret_cast<uintptr_t>(logits_dev) & (esz - 1)) ||
+      ((reinterpret_cast<uintptr_t>(cum_dev) | reinterpret_cast<uintptr_t>(tokens_dev) |
+        reinterpret_cast<uintptr_t>(parents_dev) | reinterpret_cast<uintptr_t>(scores_dev)) & 3u))
+    return fail(MK_ERR_INVALID_ARG, who, "arrays are aligned to their type");
+  const size_t need = mk_beam_select_workspace_bytes(n_batch, beams, vocab);
+  if (!workspace_dev || (reinterpret_cast<uintptr_t>(workspace_dev) & 15u) || workspace_bytes < need)
+    return fail(MK_ERR_INVALID_ARG, who, "the workspace is 16-byte aligned and of the bytes asked for");
+  SelectArgs a;
+  a.logits = logits_dev; a.stride = (size_t)row_stride * esz;
+  a.cum = cum_dev; a.finished = finished_dev;
+  a.tokens = tokens_dev; a.parents = parents_dev; a.scores = scores_dev; a.done = finished_out_dev;
+  a.dtype = dtype; a.beams = beams; a.vocab = vocab; a.eos = eos;
+  a.chunks = (vocab + kChunk - 1) / kChunk;
+  a.wide = ((reinterpret_cast<uintptr_t>(logits_dev) | a.stride) & 15u) == 0;
+  const size_t rows = (size_t)n_batch * beams;
+  a.sums = static_cast<float2*>(workspace_dev);
+  a.lists = reinterpret_cast<uint2*>(a.sums + rows * a.chunks);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = pdl_launch(beam_chunk_kernel, dim3(a.chunks, (unsigned)rows), dim3(kThreadsS), 0, st, a);
+  if (e == cudaSuccess) e = pdl_launch(beam_join_kernel, dim3(n_batch), dim3(32 * beams), 0, st, a);
+  return e == cudaSuccess ? MK_OK : fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+}
+
+extern "C" int mk_beam_reorder(void* state_dev, const int32_t* parents_dev, int n_batch, int beams,
+                               size_t beam_stride, int n_segments, size_t segment_stride,
+                               size_t segment_bytes, void* stream) {
+  const char* who = "mk_beam_reorder";
+  if (n_batch < 1 || n_batch > 32767 || beams < 1 || beams > kMaxBeams)
+    return fail(MK_ERR_INVALID_ARG, who, "1 to 16 beams and 1 to 32767 searches");
+  if (n_segments < 0 || n_segments > 65535) return fail(MK_ERR_INVALID_ARG, who, "0 to 65535 segments");
+  if (!state_dev || !parents_dev) return fail(MK_ERR_INVALID_ARG, who, "no state or parents");
+  if ((reinterpret_cast<uintptr_t>(state_dev) | beam_stride | segment_stride | segment_bytes) & 15u)
+    return fail(MK_ERR_INVALID_ARG, who, "the state, its strides and a segment's bytes are multiples of 16");
+  if (reinterpret_cast<uintptr_t>(parents_dev) & 3u) return fail(MK_ERR_INVALID_ARG, who, "parents are 4-byte aligned");
+  if (segment_bytes > (size_t)1 << 34) return fail(MK_ERR_INVALID_ARG, who, "a segment has at most 2^34 bytes");
+  if (n_segments > 1 && segment_stride < segment_bytes)
+    return fail(MK_ERR_INVALID_ARG, who, "segments of a beam do not overlap");
+  if (n_segments && n_batch * beams > 1 && beam_stride < (n_segments - 1) * segment_stride + segment_bytes &&
+      !(n_segments > 1 && segment_stride >= (size_t)(n_batch * beams - 1) * beam_stride + segment_bytes &&
+        beam_stride >= segment_bytes))
+    return fail(MK_ERR_INVALID_ARG, who, "beams do not overlap");
+  ReorderArgs a = {};
+  a.parents = parents_dev; a.beams = beams; a.n_states = 1;
+  ReorderState& s = a.state[0];
+  s.base = static_cast<uint8_t*>(state_dev);
+  s.stride = beam_stride; s.seg_stride = segment_stride;
+  s.segments = n_segments; s.count16 = (uint32_t)(segment_bytes / 16);
+  const cudaError_t e = launch_reorder(a, n_batch, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MK_OK : fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+}
+
+extern "C" int mk_kv4_reorder(const mk_kv4_cache* cache, const int32_t* parents_dev, int beams, int first,
+                              int n_keys, void* stream) {
+  const char* who = "mk_kv4_reorder";
+  if (int rc = kv4_check(cache, who)) return rc;
+  if (beams < 1 || beams > kMaxBeams || cache->n_seq % beams)
+    return fail(MK_ERR_INVALID_ARG, who, "1 to 16 beams, and whole searches of them in the cache");
+  const long long capacity = (long long)cache->pages_per_seq * cache->page_tokens;
+  if (first < 0 || n_keys < first || n_keys > capacity)
+    return fail(MK_ERR_INVALID_ARG, who, "keys [first, n_keys) of the cache");
+  if (!parents_dev || (reinterpret_cast<uintptr_t>(parents_dev) & 3u))
+    return fail(MK_ERR_INVALID_ARG, who, "parents are a 4-byte aligned array");
+  if (n_keys == first) return MK_OK;
+  const int b0 = first / kKv4Block, b1 = (n_keys + kKv4Block - 1) / kKv4Block;
+  const uint32_t block16 = kKv4Block * (cache->head_dim + cache->head_dim / 8) / 16;
+  if ((long long)b1 * block16 > 0x7FFFFFFFll) return fail(MK_ERR_INVALID_ARG, who, "too many keys in one call");
+  ReorderArgs a = {};
+  a.parents = parents_dev; a.beams = beams; a.n_states = 1;
+  ReorderState& s = a.state[0];
+  s.base = static_cast<uint8_t*>(cache->pool_dev);
+  s.table = cache->table_dev; s.pps = cache->pages_per_seq; s.pages = cache->n_pages;
+  s.page16 = cache->page_tokens / kKv4Block * block16;
+  s.seg_stride = (size_t)s.page16 * 16;
+  s.stride = s.seg_stride * cache->n_kv_heads;
+  s.segments = cache->n_kv_heads;
+  s.first16 = b0 * block16; s.count16 = (b1 - b0) * block16;
+  if (cache->scores_dev) {   // a page is a multiple of 32 keys: rows of scores are whole 16-byte columns
+    if (reinterpret_cast<uintptr_t>(cache->scores_dev) & 15u)
+      return fail(MK_ERR_INVALID_ARG, who, "scores are 16-byte aligned");
+    ReorderState& w = a.state[a.n_states++];
+    w.base = reinterpret_cast<uint8_t*>(cache->scores_dev);
+    w.seg_stride = (size_t)capacity * 4;
+    w.stride = w.seg_stride * cache->n_kv_heads;
+    w.segments = cache->n_kv_heads;
+    w.first16 = b0 * (kKv4Block / 4); w.count16 = (b1 - b0) * (kKv4Block / 4);
+  }
+  const cudaError_t e = launch_reorder(a, cache->n_seq / beams, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MK_OK : fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+}

@@ -1,0 +1,544 @@
+// kv4.cu -- the 4-bit KV cache's writers and readers: append, read, eviction.
+#include <math.h>
+#include <stdio.h>
+
+#include <type_traits>
+
+#include "kv4.cuh"
+#include "pdl.cuh"
+
+namespace mk {
+
+int kv4_fail(int code, const char* who, const char* why) {
+  char msg[256];
+  snprintf(msg, sizeof msg, "%s: %s", who, why);
+  set_last_error(msg);
+  return code;
+}
+
+int kv4_check(const mk_kv4_cache* c, const char* who) {
+  if (!c) return kv4_fail(MK_ERR_INVALID_ARG, who, "no cache");
+  if (!c->pool_dev || !c->lens_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "a cache has a pool and lengths");
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return kv4_fail(MK_ERR_UNSUPPORTED, who, "head_dim is 64 or 128");
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 1024)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "n_kv_heads is 1 to 1024");
+  if (c->page_tokens < kKv4Block || c->page_tokens % kKv4Block)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "page_tokens is a positive multiple of 32");
+  if (c->n_seq < 1 || c->n_seq > kKv4MaxSeq) return kv4_fail(MK_ERR_INVALID_ARG, who, "n_seq is 1 to 4096");
+  if (c->n_pages < 1 || c->pages_per_seq < 1)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "n_pages and pages_per_seq are positive");
+  if ((long long)c->pages_per_seq * c->page_tokens > (1ll << 30))
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "a sequence holds at most 2^30 keys");
+  if (!c->table_dev && (long long)c->n_seq * c->pages_per_seq > c->n_pages)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "without a table the pool has n_seq * pages_per_seq pages");
+  if (c->k_log2 < -32 || c->k_log2 > 32 || c->v_log2 < -32 || c->v_log2 > 32)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "k_log2 and v_log2 are -32 to 32");
+  if (reinterpret_cast<uintptr_t>(c->pool_dev) & 15u)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "the pool is 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(c->table_dev) | reinterpret_cast<uintptr_t>(c->lens_dev) |
+       reinterpret_cast<uintptr_t>(c->scores_dev)) & 3u)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "table, lengths and scores are 4-byte aligned");
+  return MK_OK;
+}
+
+Kv4 kv4_of(const mk_kv4_cache* c) {
+  Kv4 k;
+  k.pool = static_cast<uint8_t*>(c->pool_dev);
+  k.table = c->table_dev; k.lens = c->lens_dev; k.scores = c->scores_dev;
+  k.heads = c->n_kv_heads; k.page_tokens = c->page_tokens; k.pages = c->n_pages;
+  k.n_seq = c->n_seq; k.pps = c->pages_per_seq;
+  return k;
+}
+
+// ------------------------------------------------------------------ append
+
+__device__ __forceinline__ void load16(const void* p, int dtype, float (&x)[16]) {
+  if (dtype == MK_DTYPE_F32) {
+    const float4* f = static_cast<const float4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = __ldcg(f + i);
+      x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    }
+    return;
+  }
+  const uint4* u = static_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldcg(u + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      if (dtype == MK_DTYPE_BF16) {
+        a = __uint_as_float(w[j] << 16);
+        b = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        a = f.x; b = f.y;
+      }
+      x[8 * i + 2 * j] = a; x[8 * i + 2 * j + 1] = b;
+    }
+  }
+}
+
+// One group: the scale is e4m3(max |x| / 6), rounded to nearest even and at
+// most 448; a code is the e2m1 value nearest x / scale, halves to the even
+// code.  Both are decided exactly: a quotient by 6 never rounds onto a
+// midpoint of the e4m3 grid that it is not on, and x is compared with the
+// products midpoint * scale, which have at most 7 significant bits, instead of
+// a rounded quotient with the midpoints.  A NaN or infinity makes the scale
+// NaN: the whole group then reads back as NaN.
+__device__ __forceinline__ void quantize16(float (&x)[16], int neg_log2, uint2& codes, uint32_t& scale) {
+  float top = 0.f;
+  bool bad = false;
+  const float f = __int_as_float((127 + neg_log2) << 23);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+    x[i] *= f;   // a power of two; past the range it saturates below
+    top = fmaxf(top, fabsf(x[i]));
+  }
+  const float want = __fdiv_rn(top, 6.f);
+  unsigned short two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(want));
+  scale = two & 0x7Fu;
+  uint32_t hs = e4m3x2(scale);
+  const float s = __half2float(__ushort_as_half((unsigned short)(hs & 0xFFFFu)));
+  const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s,
+              t5 = 3.5f * s, t6 = 5.f * s;
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float a = fabsf(x[i]);
+    uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
+    if (s == 0.f) c = 0;
+    c |= x[i] < 0.f ? 8u : 0u;
+    w[i >> 3] |= c << (4 * (i & 7));
+  }
+  codes = make_uint2(w[0], w[1]);
+  if (bad) { scale = 0x7Fu; codes = make_uint2(0u, 0u); }
+}
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendSmemSeq = 512;   // offsets kept in shared memory up to this many sequences
+
+// One thread per 16 dims of one token's key or value (one KV head).  The
+// input is read once and 9 bytes written for its 32 or 64; threads of a warp
+// hold consecutive groups of the token, so reads are contiguous and a row's
+// codes are written as whole 32-byte sectors.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads)
+    kv4_append_kernel(Kv4 c, const uint8_t* k, const uint8_t* v, int dtype,
+                      size_t k_stride, size_t v_stride, const int32_t* offsets,
+                      int n_tokens, int k_neg, int v_neg) {
+  using S = Kv4Shape<D>;
+  __shared__ int32_t offs[kAppendSmemSeq + 1];
+  pdl_trigger();
+  pdl_wait();
+  const bool near = c.n_seq <= kAppendSmemSeq;
+  if (near) {
+    for (int i = threadIdx.x; i <= c.n_seq; i += kAppendThreads) offs[i] = __ldcg(offsets + i);
+    __syncthreads();
+  }
+  constexpr int G = D / kKv4Group;
+  const int per = c.heads * 2 * G;   // threads of a token
+  const long long id = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
+  const long long tok = id / per;
+  if (tok >= n_tokens) return;
+  int r = (int)(id - tok * per);
+  const int g = r % G;
+  r /= G;
+  const int head = r % c.heads, which = r / c.heads;
+  auto at = [&](int i) { return near ? offs[i] : __ldcg(offsets + i); };
+  int lo = 0, hi = c.n_seq;   // the last sequence whose offset is <= tok
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (mid < c.n_seq && at(mid) <= tok) lo = mid; else hi = mid - 1;
+  }
+  const int first = at(lo), end = at(lo + 1);
+  if (tok < first || tok >= end) return;   // before the first sequence or behind the last
+  const long long slot = (long long)__ldcg(c.lens + lo) - end + tok;
+  if (slot < 0 || slot >= c.capacity()) return;
+  const int lp = (int)slot / c.page_tokens, in = (int)slot - lp * c.page_tokens;
+  const int page = c.page(lo, lp);
+  if (page < 0) return;
+  const int esz = dtype == MK_DTYPE_F32 ? 4 : 2;
+  float x[16];
+  load16((which ? v + (size_t)tok * v_stride : k + (size_t)tok * k_stride) +
+             (size_t)(head * D + g * kKv4Group) * esz,
+         dtype, x);
+  uint2 codes;
+  uint32_t scale;
+  quantize16(x, which ? v_neg : k_neg, codes, scale);
+  uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
+  const int row = in % kKv4Block;
+  *reinterpret_cast<uint2*>(b + (which ? S::kVc : 0) + row * S::kCodes + g * 8) = codes;
+  b[(which ? S::kVs : S::kKs) + row * S::kScales + g] = (uint8_t)scale;
+  if (c.scores && !which && g == 0)
+    c.scores[((size_t)lo * c.heads + head) * c.capacity() + slot] = 0.f;
+}
+
+// -------------------------------------------------------------------- read
+
+__device__ __forceinline__ void store16(void* p, int dtype, const float (&x)[16]) {
+  if (dtype == MK_DTYPE_F32) {
+    float4* f = static_cast<float4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    return;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (dtype == MK_DTYPE_BF16)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+    else
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+  }
+  uint4* u = static_cast<uint4*>(p);
+  u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ __forceinline__ void widen16(uint2 codes, uint32_t scale, float mul, float (&x)[16]) {
+  const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2(scale) & 0xFFFFu))) * mul;
+  const uint32_t w[2] = {codes.x, codes.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[4];
+    e2m1x8(w[i], h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      x[8 * i + 2 * j] = f.x * s; x[8 * i + 2 * j + 1] = f.y * s;
+    }
+  }
+}
+
+constexpr int kReadThreads = 256;
+
+// One thread per 16 dims of one slot's key and value.  Groups of a row, then
+// rows of a block, run along the threads: a warp reads 256 contiguous bytes
+// of codes and writes whole rows.
+template <int D>
+__global__ void __launch_bounds__(kReadThreads)
+    kv4_read_kernel(Kv4 c, int dtype, int n, uint8_t* k_out, uint8_t* v_out,
+                    float k_mul, float v_mul) {
+  using S = Kv4Shape<D>;
+  constexpr int G = D / kKv4Group, kRows = kReadThreads / G;
+  pdl_trigger();
+  pdl_wait();
+  const int g = threadIdx.x % G;
+  const int slot = blockIdx.x * kRows + threadIdx.x / G;
+  const int head = blockIdx.y, s = blockIdx.z;
+  if (slot >= n || slot >= c.len(s)) return;
+  const int lp = slot / c.page_tokens, in = slot - lp * c.page_tokens;
+  const int page = c.page(s, lp);
+  if (page < 0) return;
+  const uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
+  const int row = in % kKv4Block;
+  const uint2 kc = *reinterpret_cast<const uint2*>(b + row * S::kCodes + g * 8);
+  const uint2 vc = *reinterpret_cast<const uint2*>(b + S::kVc + row * S::kCodes + g * 8);
+  const uint32_t ks = b[S::kKs + row * S::kScales + g], vs = b[S::kVs + row * S::kScales + g];
+  const size_t at = ((((size_t)s * n + slot) * c.heads + head) * D + g * kKv4Group) *
+                    (dtype == MK_DTYPE_F32 ? 4 : 2);
+  float x[16];
+  widen16(kc, ks, k_mul, x);
+  store16(k_out + at, dtype, x);
+  widen16(vc, vs, v_mul, x);
+  store16(v_out + at, dtype, x);
+}
+
+// ---------------------------------------------------------------- eviction
+
+// fp32 to an integer of the same order; NaN lowest, both zeros equal.
+__device__ __forceinline__ uint32_t score_key(float f) {
+  if (f != f) return 0u;
+  if (f == 0.f) return 0x80000000u;
+  const uint32_t b = __float_as_uint(f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+
+// Sum of one value per thread over the block, to every thread.  `buf` holds
+// two rows that calls alternate between, so one barrier a call is enough.
+__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*buf)[kSelWarps], int& flip) {
+  v = __reduce_add_sync(0xFFFFFFFFu, v);
+  if ((threadIdx.x & 31) == 0) buf[flip][threadIdx.x >> 5] = v;
+  __syncthreads();
+  const uint32_t t = __reduce_add_sync(0xFFFFFFFFu, buf[flip][threadIdx.x & 31]);
+  flip ^= 1;
+  return t;
+}
+
+// Which slots a head keeps.  One CTA per (sequence, KV head): the `take`
+// highest scores between the protected ends.  The threshold -- the highest T
+// with at least `take` keys >= T -- is found bit by bit from the top, each bit
+// one count over the keys, which stay in registers up to KPT * 1024 of them
+// (longer heads read theirs from L2 again for each bit).  A histogram per
+// digit would need fewer passes, but accumulated weights share their
+// exponents, so its shared-memory adds would run one after another on a few
+// bins.  The search stops at the first T with exactly `take` keys above.
+// Slots above T, and the lowest of those on it, are then written in slot
+// order by one prefix sum: position = (# above before) + min(# equal before,
+// equals wanted).
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads, 1)
+    kv4_select_kernel(Kv4 c, int budget, int first, int last, int32_t* kept) {
+  __shared__ uint32_t sums[2][kSelWarps];
+  __shared__ uint32_t cnt[KPT][kSelWarps];
+  __shared__ uint32_t carry[2];
+  pdl_trigger();
+  pdl_wait();
+  const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int n = c.len(s);
+  int32_t* out = kept + ((size_t)s * c.heads + head) * budget;
+  if (n <= budget) {
+    for (int i = tid; i < budget; i += kSelThreads) out[i] = i < n ? i : -1;
+    return;
+  }
+  const float* sc = c.scores + ((size_t)s * c.heads + head) * c.capacity() + first;
+  const int m = n - first - last, take = budget - first - last;   // take < m
+  for (int i = tid; i < first; i += kSelThreads) out[i] = i;
+  for (int i = tid; i < last; i += kSelThreads) out[budget - last + i] = n - last + i;
+  if (take == 0) return;
+  const bool whole = m <= KPT * kSelThreads;
+  uint32_t key[KPT];
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int i = j * kSelThreads + tid;
+    key[j] = whole && i < m ? score_key(__ldcg(sc + i)) : 0u;
+  }
+  int flip = 0;
+  // keys >= t (t > 0, so the padding zeros never count)
+  auto at_least = [&](uint32_t t) {
+    uint32_t v = 0;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) v += key[j] >= t;
+    } else {
+      for (int i = tid; i < m; i += kSelThreads) v += score_key(__ldcg(sc + i)) >= t;
+    }
+    return block_sum(v, sums, flip);
+  };
+  uint32_t T = 0, have = (uint32_t)m;
+  for (int bit = 31; bit >= 0 && have != (uint32_t)take; --bit) {
+    const uint32_t t = T | (1u << bit), a = at_least(t);
+    if (a >= (uint32_t)take) { T = t; have = a; }
+  }
+  // `have` keys are >= T.  Exactly `take`: all of them are kept and none is on
+  // the border; otherwise T is a key's value and the lowest slots on it fill up.
+  uint32_t above = have;
+  const bool exact = have == (uint32_t)take;
+  if (!exact) above = T == 0xFFFFFFFFu ? 0u : at_least(T + 1u);
+  const uint32_t equals = exact ? 0u : (uint32_t)take - above;
+  if (tid == 0) carry[0] = carry[1] = 0u;
+  for (int base = 0; base < m; base += KPT * kSelThreads) {
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) {
+        const int i = base + j * kSelThreads + tid;
+        key[j] = i < m ? score_key(__ldcg(sc + i)) : 0u;
+      }
+    }
+    uint32_t gt = 0, eq = 0;   // a bit per j
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const bool in = base + j * kSelThreads + tid < m;
+      const bool g = in && (exact ? key[j] >= T : key[j] > T), e = in && !exact && key[j] == T;
+      gt |= (uint32_t)g << j;
+      eq |= (uint32_t)e << j;
+      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, g), be = __ballot_sync(0xFFFFFFFFu, e);
+      if (lane == 0) cnt[j][warp] = (uint32_t)__popc(bg) << 16 | (uint32_t)__popc(be);
+    }
+    __syncthreads();
+    // exclusive prefix over (j, warp), counts above in the high half (at most 32,768 of each)
+    const bool mine = tid < KPT * kSelWarps;
+    const uint32_t own = mine ? cnt[tid >> 5][lane] : 0u;
+    uint32_t inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) sums[flip][warp] = inc;
+    __syncthreads();
+    uint32_t before = lane < warp ? sums[flip][lane] : 0u;
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if (mine) cnt[tid >> 5][lane] = before + inc - own;
+    const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, sums[flip][lane]);
+    flip ^= 1;
+    const uint32_t cg = carry[0], ce = carry[1];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt >> j & 1u),
+                     be = __ballot_sync(0xFFFFFFFFu, eq >> j & 1u);
+      const uint32_t lt = (1u << lane) - 1u, p = cnt[j][warp];
+      const uint32_t ng = cg + (p >> 16) + __popc(bg & lt), ne = ce + (p & 0xFFFFu) + __popc(be & lt);
+      if ((gt >> j & 1u) || ((eq >> j & 1u) && ne < equals))
+        out[first + ng + min(ne, equals)] = first + base + j * kSelThreads + tid;
+    }
+    if (tid == 0) { carry[0] = cg + (all >> 16); carry[1] = ce + (all & 0xFFFFu); }
+    __syncthreads();
+  }
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveLanes = 8;    // threads of a row
+constexpr int kMoveRows = 4;     // rows of a thread, their loads in flight together
+
+// Copies the kept rows to their place in the other cache: 8 threads a row, 16
+// (d = 128) or 8 bytes of codes each, the scales beside the first of K and V.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads)
+    kv4_move_kernel(Kv4 src, Kv4 dst, int budget, const int32_t* kept) {
+  using S = Kv4Shape<D>;
+  using Code = typename std::conditional<D == 128, uint4, uint2>::type;
+  using Scale = typename std::conditional<D == 128, uint2, uint32_t>::type;
+  constexpr int kPer = kMoveThreads / kMoveLanes;
+  pdl_trigger();
+  pdl_wait();
+  const int head = blockIdx.y, s = blockIdx.z;
+  const int t = threadIdx.x % kMoveLanes, which = t / 4, piece = t % 4;
+  const int32_t* list = kept + ((size_t)s * src.heads + head) * budget;
+  const size_t row_of_scores = (size_t)s * src.heads + head;
+  int from[kMoveRows], to[kMoveRows];
+  Code code[kMoveRows];
+  Scale scale[kMoveRows];
+  float score[kMoveRows];
+#pragma unroll
+  for (int i = 0; i < kMoveRows; ++i) {
+    to[i] = (blockIdx.x * kMoveRows + i) * kPer + threadIdx.x / kMoveLanes;
+    from[i] = to[i] < budget ? __ldcg(list + to[i]) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kMoveRows; ++i) {
+    if (from[i] < 0 || from[i] >= src.capacity()) { from[i] = -1; continue; }
+    const int lp = from[i] / src.page_tokens, in = from[i] - lp * src.page_tokens;
+    const int page = src.page(s, lp);
+    if (piece == 1 && which == 0 && src.scores) score[i] = __ldcg(src.scores + row_of_scores * src.capacity() + from[i]);
+    if (page < 0) { from[i] = -2; continue; }
+    const uint8_t* b = kv4_block<D>(src, page, head, in / kKv4Block);
+    const int row = in % kKv4Block;
+    code[i] = __ldcg(reinterpret_cast<const Code*>(b + (which ? S::kVc : 0) + row * S::kCodes) + piece);
+    if (piece == 0) scale[i] = __ldcg(reinterpret_cast<const Scale*>(b + (which ? S::kVs : S::kKs) + row * S::kScales));
+  }
+#pragma unroll
+  for (int i = 0; i < kMoveRows; ++i) {
+    if (from[i] == -1 || to[i] >= dst.capacity()) continue;
+    if (piece == 1 && which == 0 && dst.scores) dst.scores[row_of_scores * dst.capacity() + to[i]] = src.scores ? score[i] : 0.f;
+    const int lp = to[i] / dst.page_tokens, in = to[i] - lp * dst.page_tokens;
+    const int page = dst.page(s, lp);
+    if (page < 0 || from[i] == -2) continue;
+    uint8_t* b = kv4_block<D>(dst, page, head, in / kKv4Block);
+    const int row = in % kKv4Block;
+    *(reinterpret_cast<Code*>(b + (which ? S::kVc : 0) + row * S::kCodes) + piece) = code[i];
+    if (piece == 0) *reinterpret_cast<Scale*>(b + (which ? S::kVs : S::kKs) + row * S::kScales) = scale[i];
+  }
+}
+
+static int dtype_bytes(int dtype) {
+  return dtype == MK_DTYPE_F32 ? 4 : (dtype == MK_DTYPE_BF16 || dtype == MK_DTYPE_F16) ? 2 : 0;
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" size_t mk_kv4_page_bytes(int n_kv_heads, int head_dim, int page_tokens) {
+  if (n_kv_heads < 1 || n_kv_heads > 1024 || (head_dim != 64 && head_dim != 128) ||
+      page_tokens < kKv4Block || page_tokens % kKv4Block)
+    return 0;
+  return (size_t)n_kv_heads * page_tokens * (head_dim + head_dim / 8);
+}
+
+extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const void* v_dev, int dtype,
+                             long long k_stride, long long v_stride, const int32_t* offsets_dev,
+                             int n_tokens, void* stream) {
+  const char* who = "mk_kv4_append";
+  if (int rc = kv4_check(cache, who)) return rc;
+  const int esz = dtype_bytes(dtype);
+  if (!esz) return kv4_fail(MK_ERR_INVALID_ARG, who, "dtype is one of MK_DTYPE_*");
+  if (n_tokens < 0) return kv4_fail(MK_ERR_INVALID_ARG, who, "n_tokens is not negative");
+  if (!offsets_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no offsets");
+  if (n_tokens == 0) return MK_OK;
+  if (!k_dev || !v_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no keys or values");
+  const long long row = (long long)cache->n_kv_heads * cache->head_dim;
+  if (k_stride < row || v_stride < row || k_stride > (1ll << 40) || v_stride > (1ll << 40))
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "a token's stride is at least n_kv_heads * head_dim");
+  if (((reinterpret_cast<uintptr_t>(k_dev) | reinterpret_cast<uintptr_t>(v_dev)) & 15u) ||
+      (k_stride * esz) % 16 || (v_stride * esz) % 16)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "keys and values of a token are 16-byte aligned");
+  const Kv4 c = kv4_of(cache);
+  const long long threads = (long long)n_tokens * c.heads * 2 * (cache->head_dim / kKv4Group);
+  const long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
+  if (blocks > 0x7FFFFFFFll) return kv4_fail(MK_ERR_INVALID_ARG, who, "too many tokens in one call");
+  const uint8_t* k = static_cast<const uint8_t*>(k_dev);
+  const uint8_t* v = static_cast<const uint8_t*>(v_dev);
+  const size_t ks = (size_t)k_stride * esz, vs = (size_t)v_stride * esz;
+  auto kernel = cache->head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>;
+  const cudaError_t e = pdl_launch(kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0,
+                                   static_cast<cudaStream_t>(stream), c, k, v, dtype, ks, vs, offsets_dev,
+                                   n_tokens, -cache->k_log2, -cache->v_log2);
+  return e == cudaSuccess ? MK_OK : kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+}
+
+extern "C" int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, void* v_out_dev,
+                           void* stream) {
+  const char* who = "mk_kv4_read";
+  if (int rc = kv4_check(cache, who)) return rc;
+  if (!dtype_bytes(dtype)) return kv4_fail(MK_ERR_INVALID_ARG, who, "dtype is one of MK_DTYPE_*");
+  if (n < 0) return kv4_fail(MK_ERR_INVALID_ARG, who, "n is not negative");
+  if (n == 0) return MK_OK;
+  if (!k_out_dev || !v_out_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no outputs");
+  if ((reinterpret_cast<uintptr_t>(k_out_dev) | reinterpret_cast<uintptr_t>(v_out_dev)) & 15u)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "outputs are 16-byte aligned");
+  const Kv4 c = kv4_of(cache);
+  const int rows = kReadThreads / (cache->head_dim / kKv4Group);
+  const int most = n < c.capacity() ? n : c.capacity();
+  auto kernel = cache->head_dim == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
+  const cudaError_t e = pdl_launch(kernel, dim3((unsigned)((most + rows - 1) / rows), c.heads, c.n_seq),
+                                   dim3(kReadThreads), 0, static_cast<cudaStream_t>(stream), c, dtype, n,
+                                   static_cast<uint8_t*>(k_out_dev), static_cast<uint8_t*>(v_out_dev),
+                                   ldexpf(1.f, cache->k_log2), ldexpf(1.f, cache->v_log2));
+  return e == cudaSuccess ? MK_OK : kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+}
+
+extern "C" int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, int budget, int keep_first,
+                            int keep_last, int32_t* kept_dev, void* stream) {
+  const char* who = "mk_kv4_evict";
+  if (int rc = kv4_check(src, who)) return rc;
+  if (int rc = kv4_check(dst, who)) return rc;
+  if (src->n_kv_heads != dst->n_kv_heads || src->head_dim != dst->head_dim || src->n_seq != dst->n_seq ||
+      src->k_log2 != dst->k_log2 || src->v_log2 != dst->v_log2)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "both caches have the same heads, head_dim, sequences and log2");
+  if (!src->scores_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "the source has scores");
+  if (budget < 1 || budget > (long long)dst->pages_per_seq * dst->page_tokens)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "budget is 1 to the destination's capacity");
+  if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > budget)
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "keep_first + keep_last is 0 to budget");
+  if (!kept_dev || (reinterpret_cast<uintptr_t>(kept_dev) & 3u))
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "kept is a 4-byte aligned array");
+  if (dst->scores_dev == src->scores_dev ||
+      (src->pool_dev == dst->pool_dev && src->table_dev == dst->table_dev))
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "the destination has pages and scores of its own");
+  const Kv4 a = kv4_of(src), b = kv4_of(dst);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // as many registers of keys as the longest head can need
+  auto select = a.capacity() <= 2 * kSelThreads ? kv4_select_kernel<2>
+                : a.capacity() <= 8 * kSelThreads ? kv4_select_kernel<8> : kv4_select_kernel<32>;
+  cudaError_t e = pdl_launch(select, dim3(a.heads, a.n_seq), dim3(kSelThreads), 0, st, a, budget, keep_first,
+                             keep_last, kept_dev);
+  if (e != cudaSuccess) return kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+  const int rows = kMoveThreads / kMoveLanes * kMoveRows;
+  auto move = src->head_dim == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>;
+  e = pdl_launch(move, dim3((budget + rows - 1) / rows, a.heads, a.n_seq), dim3(kMoveThreads), 0, st, a, b,
+                 budget, kept_dev);
+  return e == cudaSuccess ? MK_OK : kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
+}
