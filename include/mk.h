@@ -442,7 +442,7 @@ int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, vo
  * [n_seq * q_len][n_q_heads][head_dim], tokens q_stride elements apart, 16-byte
  * aligned; query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
  * n_q_heads / n_kv_heads <= 1024.  out_dev: the same type,
- * [n_seq][q_len][n_q_heads][head_dim].  fp32 softmax and sums; queries and
+ * [n_seq][q_len][n_q_heads][head_dim], 16-byte aligned.  fp32 softmax and sums; queries and
  * probabilities enter the products with at least 22 bits (probabilities of a
  * bf16 call 11).  A token that sees nothing gets zeros (a sequence shorter than
  * q_len, an empty one); slots without a page are not seen, and what a masked

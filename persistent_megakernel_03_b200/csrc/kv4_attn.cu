@@ -27,20 +27,21 @@
 //
 // Precision: code * scale is exact in fp16.  A query row is scaled by a power
 // of two to the top of fp16's range; bf16 and fp16 queries are then exact,
-// fp32 ones are the sum of two fp16 parts (22 bits).  Probabilities, as
-// 2^(S - max + 15) so that small ones stay normal, are one fp16 part for bf16
-// results (an error of 2^-12 beside the result's 2^-9) and two for fp16 and
-// fp32.  Scores, maxima, sums and outputs are fp32.
+// fp32 ones are the sum of two fp16 parts (22 bits).  Probabilities, biased so
+// that small ones stay normal, are one fp16 part for bf16 results (an error of
+// 2^-12 beside the result's 2^-9) and two for fp16 and fp32.  Scores, maxima,
+// sums and outputs are fp32.
 //
-// Work: a unit is a block of 32 keys of one (sequence, row tile, KV head).
-// All units of the call stand in one line, cut into equal contiguous ranges
-// for every warp of one wave of CTAs -- the ranges come from the lengths on
-// the device, so ragged batches are balanced and a graph may be replayed with
-// other lengths.  A warp keeps its own ring of blocks (cp.async, no barrier
-// between warps).  A range that ends inside a row of units leaves a partial
-// (unnormalised output, maximum, sum); the warps of a CTA merge theirs in
-// shared memory, and a second kernel merges what CTAs share and adds the
-// weights to the scores.  No atomics: results do not depend on timing.
+// Work: the blocks of 32 keys of all (sequence, row tile, KV head) items stand
+// in one line, each item preceded by a few units for what starting it costs,
+// and the line is cut into equal ranges, one for every warp of one wave of
+// CTAs -- from the lengths on the device, so ragged batches are balanced and a
+// graph may be replayed with other lengths.  A warp keeps its own ring of
+// blocks (cp.async, no barrier between warps).  A range that begins or ends
+// inside an item leaves a partial (unnormalised output, maximum, sum); the
+// warps of a CTA merge theirs in shared memory, and a second kernel merges
+// what CTAs share and adds the weights to the scores.  No atomics: results do
+// not depend on timing.
 #include <math.h>
 
 #include <type_traits>
@@ -56,7 +57,10 @@ constexpr int kThreadsA = kWarps * 32;
 constexpr int kStages = 3;        // blocks of a warp's ring
 constexpr int kMaxCtas = 320;     // partials are laid out for this many CTAs
 constexpr int kMaxRows = 1024;    // query rows of a KV head: q_len * group
-constexpr float kBias = 15.f;     // probabilities are 2^(S - max + kBias)
+// Probabilities are 2^(S - ref + kBias), S at most kSlack above the reference:
+// fp16 holds up to 2^15, and down to 2^-25 of the reference without loss.
+constexpr float kBias = 11.f;
+constexpr float kSlack = 4.f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -112,90 +116,129 @@ struct AttnArgs {
   int32_t s_rows;
 };
 
+// Starting an item (its pages, its queries, its result) takes about as long as
+// this many blocks; with items of one block and no such units, a warp that got 14
+// of them ran 10 times as long as one with 14 blocks of a long item.
+constexpr int kStart = 3;
+
 // The line of units: sequence by sequence, in it row tile by row tile, KV head
-// by KV head, block by block.
+// by KV head: kStart units, then the item's blocks.
 struct Line {
-  long long total;   // units
-  int ctas;          // CTAs that have any: at least kWarps units each, one a warp
+  int32_t total, each, rest;   // units; per range, and ranges that get one more
+  int32_t ctas;                // CTAs that have any: kWarps units each, or all
+  __device__ __forceinline__ int cut(int i) const { return each * i + min(i, rest); }
+  // range that holds unit u
+  __device__ __forceinline__ int range_of(int u) const {
+    const int big = (each + 1) * rest;
+    return u < big ? u / (each + 1) : rest + (u - big) / each;
+  }
+  __device__ __forceinline__ int cta_of(int u) const { return range_of(u) / kWarps; }
 };
 
 __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / kKv4Block; }
-__device__ __forceinline__ long long cut(const Line& l, int i, int parts) { return l.total * i / parts; }
+__device__ __forceinline__ int units_of(int n) { return n ? blocks_of(n) + kStart : 0; }
 
-// Sums the sequences' units over the CTA: every thread holds a run of
-// consecutive sequences, `base` the units before them.
-template <int THREADS>
-__device__ __forceinline__ void line_scan(const AttnArgs& a, Line& l, long long& base, long long& mine, int& s0,
-                                          int& s1) {
-  __shared__ long long warp_sum[THREADS / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int run = (a.c.n_seq + THREADS - 1) / THREADS;
-  s0 = min(a.c.n_seq, (int)threadIdx.x * run);
-  s1 = min(a.c.n_seq, s0 + run);
-  mine = 0;
-  for (int s = s0; s < s1; ++s) mine += blocks_of(a.c.len(s));
-  mine *= (long long)a.tiles * a.c.heads;
-  long long inc = mine;
+// One warp's view of the line: lane i holds a run of consecutive sequences, `base`
+// the units before them.
+struct Scan {
+  int32_t s0, s1, base, mine;
+};
+
+__device__ __forceinline__ Scan line_scan(const AttnArgs& a, Line& l) {
+  const int lane = threadIdx.x & 31;
+  const int run = (a.c.n_seq + 31) >> 5, items = a.tiles * a.c.heads;
+  Scan z;
+  z.s0 = min(a.c.n_seq, lane * run);
+  z.s1 = min(a.c.n_seq, z.s0 + run);
+  z.mine = 0;
+#pragma unroll 4
+  for (int s = z.s0; s < z.s1; ++s) z.mine += units_of(a.c.len(s));
+  z.mine *= items;
+  int inc = z.mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += up;
   }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  base = inc - mine;
-  l.total = 0;
+  z.base = inc - z.mine;
+  l.total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+  const int want = (l.total + kWarps - 1) / kWarps;
+  l.ctas = min(want, a.max_ctas);
+  const int parts = max(l.ctas * kWarps, 1);
+  l.each = l.total / parts;
+  l.rest = l.total - l.each * parts;
+  return z;
+}
+
+// The sequence that unit u lies in, and the units before it.
+__device__ __forceinline__ void line_find(const AttnArgs& a, const Scan& z, int u, int& seq, int& start) {
+  const bool here = u >= z.base && u < z.base + z.mine;
+  int s = z.s0, b = z.base;
+  if (here) {
+    const int items = a.tiles * a.c.heads;
+    for (; s + 1 < z.s1; ++s) {
+      const int n = units_of(a.c.len(s)) * items;
+      if (u < b + n) break;
+      b += n;
+    }
+  }
+  const int who = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+  seq = __shfl_sync(0xFFFFFFFFu, s, max(who, 0));
+  start = __shfl_sync(0xFFFFFFFFu, b, max(who, 0));
+}
+
+// Four (or N) consecutive output elements, rounded once.
+template <int DT, int N>
+__device__ __forceinline__ void store_out(uint8_t* out, size_t at, const float (&x)[N]) {
+  if (DT == MK_DTYPE_F32) {
+    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at);
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) base += warp_sum[w];
-    l.total += warp_sum[w];
+    for (int i = 0; i < N / 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  } else {
+    uint2* p = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (DT == MK_DTYPE_BF16)
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[4 * i + 2 * j + 1]), "f"(x[4 * i + 2 * j]));
+        else
+          w[j] = pack_half2(x[4 * i + 2 * j], x[4 * i + 2 * j + 1]);
+      }
+      p[i] = make_uint2(w[0], w[1]);
+    }
   }
-  const long long want = (l.total + kWarps - 1) / kWarps;
-  l.ctas = (int)(want < a.max_ctas ? want : a.max_ctas);
 }
 
-// If unit u lies in this thread's run of sequences: its sequence and the units before that sequence.
-__device__ __forceinline__ bool line_find(const AttnArgs& a, long long u, long long base, long long mine, int s0,
-                                          int s1, int& seq, long long& start) {
-  if (u < base || u >= base + mine) return false;
-  for (int s = s0; s < s1; ++s) {
-    const long long n = (long long)blocks_of(a.c.len(s)) * a.tiles * a.c.heads;
-    if (u < base + n) { seq = s; start = base; return true; }
-    base += n;
-  }
-  return false;
-}
-
-template <int R>
-__device__ __forceinline__ bool row_of(const AttnArgs& a, int tile, int n, int& token, int& head) {
-  const int row = tile * R + n;
-  token = row / a.group;
-  head = row - token * a.group;
+// Element offset of an output row, false behind the last.
+template <int D, int R>
+__device__ __forceinline__ bool out_row(const AttnArgs& a, int seq, int tile, int kvh, int n, size_t& at) {
+  const int row = tile * R + n, token = row / a.group, head = row - token * a.group;
+  at = (((size_t)seq * a.q_len + token) * a.c.heads * a.group + (size_t)kvh * a.group + head) * D;
   return row < a.rows;
 }
 
-__device__ __forceinline__ void store_out(const AttnArgs& a, size_t at, int dtype, float x) {
-  if (dtype == MK_DTYPE_F32) reinterpret_cast<float*>(a.out)[at] = x;
-  else if (dtype == MK_DTYPE_BF16) {
-    unsigned short h;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
-    reinterpret_cast<unsigned short*>(a.out)[at] = h;
-  } else reinterpret_cast<__half*>(a.out)[at] = __float2half_rn(x);
-}
+// What a sum of weighted values is multiplied with; a row that sees nothing
+// has sum 0, NaN goes through.
+__device__ __forceinline__ float inverse(const AttnArgs& a, float sum) { return sum == 0.f ? 0.f : a.o_mul / sum; }
 
-// out and, for the scores, (max, sum) of one finished row element.
-template <int D, int DT, int R>
-__device__ __forceinline__ void finish(const AttnArgs& a, int seq, int tile, int kvh, int n, int dim, float o,
-                                       float sum) {
-  int token, head;
-  if (!row_of<R>(a, tile, n, token, head)) return;
-  const size_t at = (((size_t)seq * a.q_len + token) * a.c.heads * a.group + (size_t)kvh * a.group + head) * D + dim;
-  // a row that sees nothing has sum 0; NaN goes through
-  store_out(a, at, DT, sum == 0.f ? 0.f : o / sum * a.o_mul);
+// Weight of a partial with maximum mi under the common maximum m.
+__device__ __forceinline__ float rescale(float mi, float m) {
+  return mi == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mi - m);
 }
 
 template <int D, int R>
-__device__ __forceinline__ float* part_at(float* base, size_t i) { return base + i * ((size_t)R * (D + 2)); }
+__device__ __forceinline__ float* part_at(float* base, int i) { return base + (size_t)i * (R * (D + 2)); }
+
+__device__ __forceinline__ uint32_t scaled(uint32_t codes, __half2 s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&codes), s);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ __half2 scales2(uint32_t two) {
+  const uint32_t h = e4m3x2(two);
+  return *reinterpret_cast<const __half2*>(&h);
+}
 
 // D: head dim.  DT: MK_DTYPE_* of queries and outputs.  NT: 8-row tiles of query rows.
 template <int D, int DT, int NT>
@@ -208,121 +251,131 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   constexpr int kPart = R * (D + 2);
   static_assert(kPart * 4 <= kStages * S::kBytes, "a warp's last piece takes the place of its ring");
   extern __shared__ __align__(16) uint8_t ring_all[];
-  __shared__ int found_seq[kWarps];
-  __shared__ long long found_start[kWarps];
   // pieces that a warp leaves: [0] its first, in global memory, [1] its last, in its ring's place
-  __shared__ int piece_item[2][kWarps];    // block index in the line's items, -1: none
-  __shared__ int piece_seq[2][kWarps], piece_tile[2][kWarps], piece_head[2][kWarps];
-  __shared__ int piece_begins[2][kWarps];
+  __shared__ int piece_item[2][kWarps];    // -1: none
+  __shared__ int piece_seq[2][kWarps], piece_begins[2][kWarps];
+  __shared__ float weight[kWarps + 1][R], total[R];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
   Line line;
-  long long base, mine;
-  int s0, s1;
-  line_scan<kThreadsA>(a, line, base, mine, s0, s1);
+  const Scan scan = line_scan(a, line);
+  const int items = a.tiles * a.c.heads;
 
   // sequences without a key: their outputs are zero and no unit covers them
   for (int s = blockIdx.x; s < a.c.n_seq; s += gridDim.x) {
     if (a.c.len(s) > 0) continue;
     const size_t n = (size_t)a.rows * a.c.heads * D;
-    for (size_t i = threadIdx.x; i < n; i += kThreadsA) store_out(a, s * n + i, DT, 0.f);
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (size_t i = threadIdx.x * 4; i < n; i += kThreadsA * 4) store_out<DT, 4>(a.out, s * n + i, zero);
   }
   if ((int)blockIdx.x >= line.ctas) return;
 
   // this warp's range
-  const int parts = line.ctas * kWarps;
-  for (int w = 0; w < kWarps; ++w) {
-    const long long u = cut(line, blockIdx.x * kWarps + w, parts);
-    int seq;
-    long long start;
-    if (line_find(a, u, base, mine, s0, s1, seq, start)) { found_seq[w] = seq; found_start[w] = start; }
-  }
-  if (threadIdx.x < 2 * kWarps) piece_item[threadIdx.x / kWarps][threadIdx.x % kWarps] = -1;
-  __syncthreads();
-  long long u = cut(line, blockIdx.x * kWarps + warp, parts);
-  const long long u_end = cut(line, blockIdx.x * kWarps + warp + 1, parts);
+  int u = line.cut(blockIdx.x * kWarps + warp);
+  const int u_end = line.cut(blockIdx.x * kWarps + warp + 1);
+  int seq = 0, start = 0;
+  if (u < u_end) line_find(a, scan, u, seq, start);
+  if (lane < 2) piece_item[lane][warp] = -1;
 
   uint8_t* ring = ring_all + (size_t)warp * kStages * S::kBytes;
   const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const int per = a.c.page_tokens / kKv4Block;
 
-  int seq = u < u_end ? found_seq[warp] : 0;
-  long long start = u < u_end ? found_start[warp] : 0;
+  int n = u < u_end ? a.c.len(seq) : 0;
   while (u < u_end) {
-    // ---- the piece of one (sequence, row tile, KV head) that this range covers
-    int n = a.c.len(seq);
+    // ---- the piece of one item that this range covers
     while (n == 0) n = a.c.len(++seq);   // u < total: a sequence with keys follows
     const int nb = blocks_of(n);
-    const long long in_seq = u - start;
-    const int item = (int)(in_seq / nb), b0 = (int)(in_seq - (long long)item * nb);
+    const int item = (u - start) / (nb + kStart), item_at = start + item * (nb + kStart);
     const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
-    const int b1 = (int)(u_end - u < nb - b0 ? b0 + (u_end - u) : nb);
-    const int nblk = b1 - b0;
-    const int per = a.c.page_tokens / kKv4Block;
+    const int stop = min(u_end, item_at + nb + kStart);
+    const int b0 = max(u - item_at - kStart, 0), b1 = stop - item_at - kStart;
+    const bool last_item = item + 1 == items;
+    u = stop;
+    const bool ends = b1 == nb;
+    const int this_seq = seq, this_n = n;
+    if (ends && last_item) {
+      start += (nb + kStart) * items;
+      ++seq;
+      n = u < u_end ? a.c.len(seq) : 0;
+    }
+    if (b1 <= b0) continue;   // units of the start alone
 
-    // physical blocks, 32 at a time: lane i holds the page of block b0 + 32 k + i
-    int pages = -1, pages_from = 0;
-    auto fetch_pages = [&](int from) {
-      pages_from = from;
-      pages = from + lane < b1 ? a.c.page(seq, (from + lane) / per) : -1;
-    };
-    fetch_pages(b0);
-    auto issue = [&](int b) {   // block b into its ring slot; its page, -1 where there is none
-      if (b - pages_from >= 32) fetch_pages(b);
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, b - pages_from);
-      if (page >= 0) {
-        const uint8_t* src = kv4_block<D>(a.c, page, kvh, b % per);
-        const uint32_t dst = ring_s + (b - b0) % kStages * S::kBytes;
+    // ---- query rows: column r of each 8-row tile, 4 * KS dims from t * 4 * KS; in flight
+    // while the pages are looked up
+    constexpr int kRaw = KS * (DT == MK_DTYPE_F32 ? 1 : 2) / (DT == MK_DTYPE_F32 ? 1 : 4);
+    uint4 raw[NT][kRaw];
+    int lim[NT];
+    bool row_ok[NT];
 #pragma unroll
-        for (int i = 0; i < (S::kBytes / 16 + 31) / 32; ++i) {
-          const int at = i * 32 + lane;
-          if (S::kBytes / 16 % 32 == 0 || at < S::kBytes / 16) cp16(dst + at * 16, src + at * 16);
-        }
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = tile * R + nt * 8 + r, token = row / a.group, head = row - token * a.group;
+      row_ok[nt] = row < a.rows;
+      lim[nt] = row_ok[nt] ? max(0, min(this_n, this_n - a.q_len + token + 1)) : this_n;
+      const uint8_t* p = a.q + ((size_t)this_seq * a.q_len + token) * a.q_stride +
+                         (size_t)((kvh * a.group + head) * D + t * 4 * KS) * (DT == MK_DTYPE_F32 ? 4 : 2);
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i)
+        raw[nt][i] = row_ok[nt] ? __ldcg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+
+    // ---- the ring: block b of the item is in_page blocks into logical page lp;
+    // lane i holds the physical page of lp0 + i
+    int lp0 = b0 / per, rel = 0, in_page = b0 - lp0 * per;
+    const int lp_last = (b1 - 1) / per;
+    int pages = lp0 + lane <= lp_last ? a.c.page(this_seq, lp0 + lane) : -1;
+    int page = __shfl_sync(0xFFFFFFFFu, pages, 0);
+    uint32_t fill = ring_s;
+    auto issue = [&]() {   // the next block into the ring slot at `fill`; false where it has no page
+      if (page >= 0) {
+        const uint8_t* src = kv4_block<D>(a.c, page, kvh, in_page) + lane * 16;
+        const uint32_t dst = fill + lane * 16;
+#pragma unroll
+        for (int i = 0; i < (S::kBytes / 16 + 31) / 32; ++i)
+          if (S::kBytes / 16 % 32 == 0 || i * 32 + lane < S::kBytes / 16) cp16(dst + i * 512, src + i * 512);
       }
-      return page >= 0;
+      const bool there = page >= 0;
+      fill = fill == ring_s + (kStages - 1) * S::kBytes ? ring_s : fill + S::kBytes;
+      if (++in_page == per) {
+        in_page = 0;
+        if (++rel == 32) {
+          rel = 0;
+          lp0 += 32;
+          pages = lp0 + lane <= lp_last ? a.c.page(this_seq, lp0 + lane) : -1;
+        }
+        page = __shfl_sync(0xFFFFFFFFu, pages, rel);
+      }
+      return there;
     };
-    uint32_t have = 0;   // bit: the ring slot holds a block
+    uint32_t have = 0;   // bit i: the block i ahead of the current one has a page
     __syncwarp();        // the slots' last readers are done
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (i < nblk && issue(b0 + i)) have |= 1u << i;
+      if (b0 + i < b1 && issue()) have |= 1u << i;
       cp_commit();
     }
 
-    // ---- query rows: column n = r of each 8-row tile, 2 * KS dims from t * 2 * KS
     uint32_t qf[QP][NT][2 * KS];
     float mul[NT][2];                // S -> log2 units, for this thread's columns 2t, 2t + 1
     int limit[NT][2];                // keys those columns see
-    int see_all = n;                 // keys that every row sees
+    int see_all = this_n;            // keys that every row sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      int token, head;
-      const bool ok = row_of<R>(a, tile, nt * 8 + r, token, head);
       float x[4 * KS];
-      const uint8_t* row = a.q + ((size_t)seq * a.q_len + token) * a.q_stride;
-      const int dim0 = (kvh * a.group + head) * D + t * 4 * KS;
-      if (DT == MK_DTYPE_F32) {
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const float4 v = ok ? __ldcg(reinterpret_cast<const float4*>(row + (size_t)dim0 * 4) + i)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-          x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-        }
-      } else {
+      for (int i = 0; i < kRaw; ++i) {
+        const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
 #pragma unroll
-        for (int i = 0; i < KS / 2; ++i) {
-          const uint4 v = ok ? __ldcg(reinterpret_cast<const uint4*>(row + (size_t)dim0 * 2) + i)
-                             : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (DT == MK_DTYPE_BF16) {
-              x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-              x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-            } else {
-              const float2 f = unpack_half2(w[j]);
-              x[8 * i + 2 * j] = f.x; x[8 * i + 2 * j + 1] = f.y;
-            }
+        for (int j = 0; j < 4; ++j) {
+          if (DT == MK_DTYPE_F32) x[4 * i + j] = __uint_as_float(w[j]);
+          else if (DT == MK_DTYPE_BF16) {
+            x[(8 * i + 2 * j) % (4 * KS)] = __uint_as_float(w[j] << 16);
+            x[(8 * i + 2 * j + 1) % (4 * KS)] = __uint_as_float(w[j] & 0xFFFF0000u);
+          } else {
+            const float2 f = unpack_half2(w[j]);
+            x[(8 * i + 2 * j) % (4 * KS)] = f.x;
+            x[(8 * i + 2 * j + 1) % (4 * KS)] = f.y;
           }
         }
       }
@@ -335,7 +388,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       int e = 13 - ((__float_as_int(top) >> 23) - 127);
       e = min(max(e, -120), 120);
       const float up = __int_as_float((127 + e) << 23);
-      const float down = __int_as_float((127 - e) << 23) * a.s_mul;
+      // not 0: masked scores are -inf and their product has to stay it
+      const float down = fmaxf(__int_as_float((127 - e) << 23) * a.s_mul, 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) {
         const float f0 = x[2 * i] * up, f1 = x[2 * i + 1] * up;
@@ -346,79 +400,76 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
           qf[QP - 1][nt][i] = pack_half2(f0 - b.x, f1 - b.y);
         }
       }
-      const int lim = ok ? max(0, min(n, n - a.q_len + token + 1)) : n;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         mul[nt][c] = __shfl_sync(0xFFFFFFFFu, down, (2 * t + c) * 4);
-        limit[nt][c] = __shfl_sync(0xFFFFFFFFu, lim, (2 * t + c) * 4);
+        limit[nt][c] = __shfl_sync(0xFFFFFFFFu, lim[nt], (2 * t + c) * 4);
       }
-      see_all = min(see_all, lim);
+      see_all = min(see_all, lim[nt]);
     }
     see_all = __reduce_min_sync(0xFFFFFFFFu, see_all);
 
     float o[NT][KS][4];
-    float mx[NT][2], sum[NT][2];
+    float ref[NT][2], sum[NT][2];    // reference of the probabilities (log2 units), their sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < KS; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
-      mx[nt][0] = mx[nt][1] = -INFINITY;
+      ref[nt][0] = ref[nt][1] = -INFINITY;
       sum[nt][0] = sum[nt][1] = 0.f;
     }
+    // this thread's keys of a half block: mma rows r and r + 8
+    const int key_r = (r >> 1) + (r & 1) * 4;
+    float* s_to = a.accumulate
+                      ? a.s_all + ((size_t)(item_at + kStart + b0) * kKv4Block + key_r) * a.s_rows + 2 * t : nullptr;
+    const uint8_t* blk = ring;
 
     for (int b = b0; b < b1; ++b) {
-      const int slot = (b - b0) % kStages;
       cp_wait<kStages - 2>();
       __syncwarp();
-      {
-        const int next = b + kStages - 1, ns = (next - b0) % kStages;
-        if (next < b1) {
-          if (issue(next)) have |= 1u << ns; else have &= ~(1u << ns);
-        }
-        cp_commit();
-      }
-      const bool there = have >> slot & 1u;
-      const uint8_t* blk = ring + slot * S::kBytes;
+      if (b + kStages - 1 < b1 && issue()) have |= 1u << (kStages - 1);
+      cp_commit();
+      const bool there = have & 1u;
+      have >>= 1;
       const bool masked = !there || (b + 1) * kKv4Block > see_all;   // some row does not see some key
 
       // S^T, 16 keys at a time
       float sc[2][NT][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int ka = half * 16 + (r >> 1) + (r & 1) * 4, kb = ka + 8;   // mma rows r and r + 8
+        const int ka = half * 16 + key_r, kb = ka + 8;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[half][nt][i] = 0.f;
-        uint32_t wa[KS / 2], wb[KS / 2], sa[2], sb[2];
+        uint32_t wa[KS / 2], wb[KS / 2];
+        __half2 sa, sb;   // scales of this thread's two groups (d = 64: one)
         if (D == 128) {
           const uint4 va = *reinterpret_cast<const uint4*>(blk + ka * S::kCodes + t * 16);
           const uint4 vb = *reinterpret_cast<const uint4*>(blk + kb * S::kCodes + t * 16);
           wa[0] = va.x; wa[1] = va.y; wa[KS / 2 - 2] = va.z; wa[KS / 2 - 1] = va.w;
           wb[0] = vb.x; wb[1] = vb.y; wb[KS / 2 - 2] = vb.z; wb[KS / 2 - 1] = vb.w;
-          const uint32_t ha = e4m3x2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + ka * S::kScales + 2 * t));
-          const uint32_t hb = e4m3x2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + kb * S::kScales + 2 * t));
-          sa[0] = __byte_perm(ha, 0, 0x1010); sa[1] = __byte_perm(ha, 0, 0x3232);
-          sb[0] = __byte_perm(hb, 0, 0x1010); sb[1] = __byte_perm(hb, 0, 0x3232);
+          sa = scales2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + ka * S::kScales + 2 * t));
+          sb = scales2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + kb * S::kScales + 2 * t));
         } else {
           const uint2 va = *reinterpret_cast<const uint2*>(blk + ka * S::kCodes + t * 8);
           const uint2 vb = *reinterpret_cast<const uint2*>(blk + kb * S::kCodes + t * 8);
           wa[0] = va.x; wa[1] = va.y; wb[0] = vb.x; wb[1] = vb.y;
-          const uint32_t ha = e4m3x2(blk[S::kKs + ka * S::kScales + t]);
-          const uint32_t hb = e4m3x2(blk[S::kKs + kb * S::kScales + t]);
-          sa[0] = sa[1] = __byte_perm(ha, 0, 0x1010);
-          sb[0] = sb[1] = __byte_perm(hb, 0, 0x1010);
+          sa = scales2(blk[S::kKs + ka * S::kScales + t]);
+          sb = scales2(blk[S::kKs + kb * S::kScales + t]);
         }
 #pragma unroll
         for (int w = 0; w < KS / 2; ++w) {
           uint32_t ha[4], hb[4];
           e2m1x8(wa[w], ha);
           e2m1x8(wb[w], hb);
-          const int g = w >> 1;   // 16 dims: two words
+          // 16 dims, two words, share a scale
+          const __half2 pa = w < 2 ? __low2half2(sa) : __high2half2(sa);
+          const __half2 pb = w < 2 ? __low2half2(sb) : __high2half2(sb);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) { ha[i] = hmul2(ha[i], sa[g]); hb[i] = hmul2(hb[i], sb[g]); }
+          for (int i = 0; i < 4; ++i) { ha[i] = scaled(ha[i], pa); hb[i] = scaled(hb[i], pb); }
 #pragma unroll
           for (int p = 0; p < QP; ++p)
 #pragma unroll
@@ -429,61 +480,55 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
         }
       }
 
-      // log2 units, masks, running maximum
-      float up[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = -INFINITY;
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float& x = sc[half][nt][2 * i + c];
-              x *= mul[nt][c];
-              if (masked) {
-                const int key = b * kKv4Block + half * 16 + (r >> 1) + (r & 1) * 4 + 8 * i;
-                if (!there || key >= limit[nt][c]) x = -INFINITY;
-              }
-              m = fmaxf(m, x);
-            }
-          up[nt][c] = m;
-        }
-      if (a.accumulate) {
-        float* to = a.s_all + ((size_t)(u + (b - b0)) * kKv4Block) * a.s_rows;
+      if (masked) {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int key = half * 16 + (r >> 1) + (r & 1) * 4 + 8 * i;
+            const int key = b * kKv4Block + half * 16 + key_r + 8 * i;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (!there || key >= limit[nt][c]) sc[half][nt][2 * i + c] = -INFINITY;
+          }
+      }
+      if (a.accumulate) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               if (nt * 8 + 2 * t < a.s_rows)
-                *reinterpret_cast<float2*>(to + (size_t)key * a.s_rows + nt * 8 + 2 * t) =
-                    make_float2(sc[half][nt][2 * i], sc[half][nt][2 * i + 1]);
-          }
+                *reinterpret_cast<float2*>(s_to + (half * 16 + 8 * i) * a.s_rows + nt * 8) =
+                    make_float2(sc[half][nt][2 * i] * mul[nt][0], sc[half][nt][2 * i + 1] * mul[nt][1]);
+        s_to += kKv4Block * a.s_rows;
       }
-      bool moved = false;
+
+      // The reference of a column moves only when a score passes it by kSlack:
+      // then, and in the first block, the lanes' maxima meet.
+      float top[NT][2];
+      bool moves = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float m = up[nt][c];
-          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-          moved |= m > mx[nt][c];
-          up[nt][c] = fmaxf(m, mx[nt][c]);
+          top[nt][c] = mul[nt][c] * fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
+          moves |= top[nt][c] > ref[nt][c] + kSlack;
         }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
+      if (__any_sync(0xFFFFFFFFu, moves)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            // nothing seen so far: nothing to rescale
-            const float f = mx[nt][c] == -INFINITY ? 1.f : ex2(mx[nt][c] - up[nt][c]);
-            mx[nt][c] = up[nt][c];
+            float m = top[nt][c];
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            m = fmaxf(m, ref[nt][c]);
+            const float f = ref[nt][c] == -INFINITY ? 1.f : ex2(ref[nt][c] - m);   // nothing to rescale before the first
+            ref[nt][c] = m;
             sum[nt][c] *= f;
 #pragma unroll
             for (int j = 0; j < KS; ++j) { o[nt][j][c] *= f; o[nt][j][2 + c] *= f; }
@@ -494,13 +539,14 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       uint32_t pf[PP][2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = mx[nt][0] == -INFINITY ? 0.f : mx[nt][0] - kBias;
-        const float m1 = mx[nt][1] == -INFINITY ? 0.f : mx[nt][1] - kBias;
+        const float m0 = ref[nt][0] == -INFINITY ? 0.f : kBias - ref[nt][0];
+        const float m1 = ref[nt][1] == -INFINITY ? 0.f : kBias - ref[nt][1];
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = ex2(sc[half][nt][2 * i] - m0), p1 = ex2(sc[half][nt][2 * i + 1] - m1);
+            const float p0 = ex2(fmaf(sc[half][nt][2 * i], mul[nt][0], m0));
+            const float p1 = ex2(fmaf(sc[half][nt][2 * i + 1], mul[nt][1], m1));
             sum[nt][0] += p0;
             sum[nt][1] += p1;
             const uint32_t h = pack_half2(p0, p1);
@@ -529,16 +575,18 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
             w[i][0] = *reinterpret_cast<const uint32_t*>(row + r * 4);
             s[i] = blk[S::kVs + key * S::kScales + (r >> 1)];
           }
-          if (masked) {
-            // A value that no row sees must not count, whatever it is (a page's
-            // leftovers may be NaN, and 0 * NaN is).  One that only some rows
-            // see is NaN for those alone: it leaves the product and is set below.
-            const int at = b * kKv4Block + key;
-            const bool seen = there && at < n;
-            if (!seen || (at >= see_all && (s[i] & 0x7Fu) == 0x7Fu)) s[i] = 0u;
+        }
+        if (masked) {
+          // A value that no row sees must not count, whatever it is (a page's
+          // leftovers may be NaN, and 0 * NaN is).  One that only some rows
+          // see is NaN for those alone: it leaves the product and is set below.
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = b * kKv4Block + half * 16 + t + 4 * i;
+            if (!there || at >= this_n || (at >= see_all && (s[i] & 0x7Fu) == 0x7Fu)) s[i] = 0u;
           }
         }
-        const uint32_t s01 = e4m3x2(s[0] | s[1] << 8), s23 = e4m3x2(s[2] | s[3] << 8);
+        const __half2 s01 = scales2(s[0] | s[1] << 8), s23 = scales2(s[2] | s[3] << 8);
 #pragma unroll
         for (int x = 0; x < W; ++x) {
           // bytes j: (key 0, key 1) of an even dim, of an odd one, and the same of keys 2, 3
@@ -550,8 +598,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
           e2m1x8(e01, a0); e2m1x8(d01, a1); e2m1x8(e23, a2); e2m1x8(d23, a3);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            a0[j] = hmul2(a0[j], s01); a1[j] = hmul2(a1[j], s01);
-            a2[j] = hmul2(a2[j], s23); a3[j] = hmul2(a3[j], s23);
+            a0[j] = scaled(a0[j], s01); a1[j] = scaled(a1[j], s01);
+            a2[j] = scaled(a2[j], s23); a3[j] = scaled(a3[j], s23);
 #pragma unroll
             for (int p = 0; p < PP; ++p)
 #pragma unroll
@@ -560,11 +608,11 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
           }
         }
       }
-      if (masked && there && see_all < n) {
+      if (masked && there && see_all < this_n) {
         // NaN values among keys that only some rows see
         for (int key = 0; key < kKv4Block; ++key) {
           const int at = b * kKv4Block + key;
-          if (at < see_all || at >= n) continue;
+          if (at < see_all || at >= this_n) continue;
           if ((blk[S::kVs + key * S::kScales + (D == 128 ? r : r >> 1)] & 0x7Fu) != 0x7Fu) continue;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -576,11 +624,14 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
               }
         }
       }
+      blk = blk == ring + (kStages - 1) * S::kBytes ? ring : blk + S::kBytes;
     }
     cp_wait<0>();
     __syncwarp();
 
     // ---- the piece is done: sums over the lanes that share a column
+    const bool begins = b0 == 0;
+    float* to = ends ? part_at<D, R>(a.warp_part, blockIdx.x * kWarps + warp) : reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -589,249 +640,242 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
-        sum[nt][c] = x;
-      }
-    const bool begins = b0 == 0, ends = b1 == nb;
-    const size_t stat = ((size_t)seq * a.tiles * a.c.heads + item) * R;
-    // dims of o[.][j]: lane r holds D / 8 consecutive ones, two a tile j
-    auto dim_of = [&](int j, int i) { return r * (D / 8) + 2 * j + (i >> 1); };
-    if (begins && ends) {
+        const int col = nt * 8 + 2 * t + c;
+        // lane r holds D / 8 consecutive dims of it, two of each 16-dim tile
+        float y[D / 8];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < KS; ++j) { y[2 * j] = o[nt][j][c]; y[2 * j + 1] = o[nt][j][2 + c]; }
+        if (begins && ends) {
+          size_t at;
+          if (out_row<D, R>(a, this_seq, tile, kvh, col, at)) {
+            const float f = inverse(a, x);
 #pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            finish<D, DT, R>(a, seq, tile, kvh, nt * 8 + 2 * t + (i & 1), dim_of(j, i), o[nt][j][i], sum[nt][i & 1]);
-      if (a.accumulate && r == 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            a.stats[(stat + nt * 8 + 2 * t + c) * 2] = mx[nt][c];
-            a.stats[(stat + nt * 8 + 2 * t + c) * 2 + 1] = sum[nt][c];
+            for (int i = 0; i < D / 8; ++i) y[i] *= f;
+            store_out<DT, D / 8>(a.out, at + r * (D / 8), y);
           }
-      }
-    } else {
-      const int last = !ends;
-      float* to = last ? reinterpret_cast<float*>(ring)
-                       : part_at<D, R>(a.warp_part, (size_t)blockIdx.x * kWarps + warp);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) to[(nt * 8 + 2 * t + (i & 1)) * D + dim_of(j, i)] = o[nt][j][i];
-        if (r == 0) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            to[R * D + nt * 8 + 2 * t + c] = mx[nt][c];
-            to[R * D + R + nt * 8 + 2 * t + c] = sum[nt][c];
+          if (a.accumulate && r == 0) {
+            float2* st = reinterpret_cast<float2*>(a.stats) + ((size_t)this_seq * items + item) * R + col;
+            *st = make_float2(ref[nt][c], x);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            *reinterpret_cast<float4*>(to + col * D + r * (D / 8) + 4 * i) =
+                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          if (r == 0) { to[R * D + col] = ref[nt][c]; to[R * D + R + col] = x; }
         }
       }
-      if (lane == 0) {
-        piece_item[last][warp] = (int)((size_t)seq * a.tiles * a.c.heads + item);
-        piece_seq[last][warp] = seq;
-        piece_tile[last][warp] = tile;
-        piece_head[last][warp] = kvh;
-        piece_begins[last][warp] = begins;
-      }
-    }
-    u += nblk;
-    if (ends && item + 1 == a.tiles * a.c.heads) {
-      start += (long long)nb * a.tiles * a.c.heads;
-      ++seq;
+    if (lane == 0 && !(begins && ends)) {
+      const int last = !ends;
+      piece_item[last][warp] = item;
+      piece_seq[last][warp] = this_seq;
+      piece_begins[last][warp] = begins;
     }
   }
   __syncthreads();
 
-  // ---- pieces of the CTA's warps that belong together, in order: the last
-  // of a warp, those of warps that lie whole in the item, the first of the one
+  // ---- pieces of the CTA's warps that belong together, in order: the last of
+  // a warp, those of warps that lie whole in the item, the first of the one
   // where it ends
-  int from[kWarps + 1], count = 0, item = -1, begins = 0, who = 0;
-  auto piece = [&](int code) -> const float* {
+  auto piece = [&](int code) -> const float* {   // code: 2 * warp + last
     const int w = code >> 1;
     return code & 1 ? reinterpret_cast<const float*>(ring_all + (size_t)w * kStages * S::kBytes)
-                    : part_at<D, R>(a.warp_part, (size_t)blockIdx.x * kWarps + w);
+                    : part_at<D, R>(a.warp_part, blockIdx.x * kWarps + w);
   };
-  auto merge = [&](bool ends) {
-    const int seq = piece_seq[who & 1][who >> 1], tile = piece_tile[who & 1][who >> 1],
-              kvh = piece_head[who & 1][who >> 1];
-    float* slot = part_at<D, R>(a.cta_part, (size_t)blockIdx.x * 2 + (ends ? 0 : 1));
-    for (int e = threadIdx.x; e < R * D; e += kThreadsA) {
-      const int row = e / D;
-      float m = -INFINITY;
-#pragma unroll
-      for (int i = 0; i <= kWarps; ++i)
-        if (i < count) m = fmaxf(m, piece(from[i])[R * D + row]);
-      float x = 0.f, l = 0.f;
-#pragma unroll
-      for (int i = 0; i <= kWarps; ++i)
-        if (i < count) {
-          const float* p = piece(from[i]);
-          const float mi = p[R * D + row], f = mi == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mi - m);
-          x = fmaf(f, p[e], x);
-          l = fmaf(f, p[R * D + R + row], l);
-        }
-      const bool one = e - row * D == 0;
+  // pieces `first`, then the last ones of the warps after it, `count` in all, the
+  // final one the first piece of its warp if the item ends here
+  auto merge = [&](int first, int count, bool ends) {
+    const int w0 = first >> 1, fin = ends ? 2 * (w0 + count - 1) : 2 * (w0 + count - 1) + 1;
+    const int seq = piece_seq[first & 1][w0], item = piece_item[first & 1][w0];
+    const bool begins = piece_begins[first & 1][w0];
+    const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
+    const int rows = min(R, a.rows - tile * R);
+    auto nth = [&](int i) { return piece(i == count - 1 && count > 1 ? fin : i == 0 ? first : 2 * (w0 + i) + 1); };
+    float* slot = part_at<D, R>(a.cta_part, blockIdx.x * 2 + (ends ? 0 : 1));
+    __syncthreads();   // the last merge is done with the weights
+    if ((int)threadIdx.x < R) {
+      const int row = threadIdx.x;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < count; ++i) m = fmaxf(m, nth(i)[R * D + row]);
+      for (int i = 0; i < count; ++i) {
+        const float f = rescale(nth(i)[R * D + row], m);
+        weight[i][row] = f;
+        l = fmaf(f, nth(i)[R * D + R + row], l);
+      }
+      total[row] = l;
       if (begins && ends) {
-        finish<D, DT, R>(a, seq, tile, kvh, row, e - row * D, x, l);
-        if (one && a.accumulate) {
-          a.stats[((size_t)item * R + row) * 2] = m;
-          a.stats[((size_t)item * R + row) * 2 + 1] = l;
-        }
+        if (a.accumulate)
+          reinterpret_cast<float2*>(a.stats)[((size_t)seq * items + item) * R + row] = make_float2(m, l);
       } else {
-        slot[e] = x;
-        if (one) { slot[R * D + row] = m; slot[R * D + R + row] = l; }
+        slot[R * D + row] = m;
+        slot[R * D + R + row] = l;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < rows * D; e += kThreadsA * 4) {
+      const int row = e / D;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < count; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(nth(i) + e);
+        const float f = weight[i][row];
+        x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]);
+        x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+      }
+      if (begins && ends) {
+        size_t at;
+        out_row<D, R>(a, seq, tile, kvh, row, at);
+        const float f = inverse(a, total[row]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] *= f;
+        store_out<DT, 4>(a.out, at + e - row * D, x);
+      } else {
+        *reinterpret_cast<float4*>(slot + e) = make_float4(x[0], x[1], x[2], x[3]);
       }
     }
   };
+  int open = -1, count = 0;
 #pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-#pragma unroll
-    for (int last = 0; last < 2; ++last) {
-      const int it = piece_item[last][w];
-      if (it < 0) continue;
-      if (count == 0) { item = it; begins = piece_begins[last][w]; who = 2 * w + last; }
-      from[count++] = 2 * w + last;
-      if (!last) { merge(true); count = 0; }
-    }
+  for (int code = 0; code < 2 * kWarps; ++code) {
+    const int last = code & 1;
+    if (piece_item[last][code >> 1] < 0) continue;
+    if (count == 0) open = code;
+    ++count;
+    if (!last) { merge(open, count, true); count = 0; }
   }
-  if (count) merge(false);
+  if (count) merge(open, count, false);
 }
 
-// ---- what CTAs share: the first CTA boundary inside an item merges its
-// pieces; then, if asked, every key's weights go to its score.
-constexpr int kThreadsM = 512;
+// ---- what CTAs share.  The CTAs whose ranges begin strictly inside an item
+// split its merge among them; then, if asked, every key's weights go to its
+// score.
+constexpr int kThreadsM = 256;
+constexpr int kWarpsM = kThreadsM / 32;
 
 template <int D, int DT, int R>
-__global__ void __launch_bounds__(kThreadsM, 1) kv4_attn_merge_kernel(const AttnArgs a) {
-  __shared__ int f_seq[3];
-  __shared__ long long f_start[3];
-  __shared__ float stat_m[kMaxRows], stat_l[kMaxRows];
+__global__ void __launch_bounds__(kThreadsM) kv4_attn_merge_kernel(const AttnArgs a) {
+  __shared__ float2 stat[kMaxRows];
   pdl_trigger();
   pdl_wait();
   Line line;
-  long long base, mine;
-  int s0, s1;
-  line_scan<kThreadsM>(a, line, base, mine, s0, s1);
+  const Scan scan = line_scan(a, line);
   if (line.total == 0) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per_item = a.tiles * a.c.heads;
-  // units of all row tiles share their keys: scores go by (sequence, KV head, block)
-  const long long keys_total = line.total / a.tiles;
-  const long long v0 = keys_total * blockIdx.x / gridDim.x, v1 = keys_total * (blockIdx.x + 1) / gridDim.x;
-  const int c = blockIdx.x + 1;   // the boundary between CTAs c - 1 and c
-  const int parts = line.ctas * kWarps;
-  const long long edge = c < line.ctas ? cut(line, c * kWarps, parts) : -1;
-  {
-    const long long u[2] = {edge, v0 < v1 && a.accumulate ? v0 * a.tiles : -1};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int seq;
-      long long start;
-      if (u[i] >= 0 && line_find(a, u[i], base, mine, s0, s1, seq, start)) { f_seq[i] = seq; f_start[i] = start; }
-    }
-  }
-  __syncthreads();
-
-  // CTA whose range holds unit u
-  auto cta_of = [&](long long u) {
-    int i = (int)(((double)u + 0.5) * line.ctas / line.total);
-    i = min(max(i, 0), line.ctas - 1);
-    while (i > 0 && u < cut(line, i * kWarps, parts)) --i;
-    while (i + 1 < line.ctas && u >= cut(line, (i + 1) * kWarps, parts)) ++i;
-    return i;
-  };
+  const int items = a.tiles * a.c.heads;
   // a CTA's piece of an item that goes on behind it is its last, else its first
-  auto slot_of = [&](int cta, int c1) { return part_at<D, R>(a.cta_part, (size_t)cta * 2 + (cta < c1 ? 1 : 0)); };
+  auto slot_of = [&](int cta, int c1) { return part_at<D, R>(a.cta_part, cta * 2 + (cta < c1 ? 1 : 0)); };
 
-  if (edge >= 0) {
-    const int seq = f_seq[0], nb = blocks_of(a.c.len(seq));
-    const long long in_seq = edge - f_start[0];
-    const int item = (int)(in_seq / nb);
-    const long long i0 = f_start[0] + (long long)item * nb, i1 = i0 + nb;
-    // strictly inside, and the first such boundary of the item
-    if (edge > i0 && cut(line, (c - 1) * kWarps, parts) <= i0) {
-      const int c0 = c - 1, c1 = cta_of(i1 - 1);
+  if ((int)blockIdx.x + 1 < line.ctas) {
+    const int edge = line.cut((blockIdx.x + 1) * kWarps);   // where the next CTA begins
+    int seq, start;
+    line_find(a, scan, edge, seq, start);
+    const int nb = blocks_of(a.c.len(seq));
+    const int item = (edge - start) / (nb + kStart), i0 = start + item * (nb + kStart) + kStart;
+    if (edge > i0) {
+      const int c0 = line.cta_of(i0), c1 = line.cta_of(i0 + nb - 1);   // c0 <= blockIdx.x < c1
       const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
-      for (int e = tid; e < R * D; e += kThreadsM) {
-        const int row = e / D;
-        float m = -INFINITY, x = 0.f, l = 0.f;
-        for (int i = c0; i <= c1; ++i) m = fmaxf(m, __ldcg(slot_of(i, c1) + R * D + row));
-#pragma unroll 4
-        for (int i = c0; i <= c1; ++i) {
-          const float* p = slot_of(i, c1);
-          const float mi = __ldcg(p + R * D + row), f = mi == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mi - m);
-          x = fmaf(f, __ldcg(p + e), x);
-          l = fmaf(f, __ldcg(p + R * D + R + row), l);
+      const int fours = min(R, a.rows - tile * R) * D / 4, share = c1 - c0, me = blockIdx.x - c0;
+      const int e0 = fours * me / share, e1 = fours * (me + 1) / share;
+      // `wide` lanes to four elements, a partial each
+      int wide = 1;
+      while (wide < 32 && wide < c1 - c0 + 1) wide <<= 1;
+      const int sub = lane & (wide - 1), at_once = kWarpsM * (32 / wide);
+      for (int base = e0; base < e1; base += at_once) {   // the same number of rounds for every lane
+        const int e = base + warp * (32 / wide) + lane / wide;
+        const bool ok = e < e1;
+        const int row = ok ? e * 4 / D : 0;
+        float m = -INFINITY;
+        for (int i = c0 + sub; i <= c1; i += wide) m = fmaxf(m, __ldcg(slot_of(i, c1) + R * D + row));
+        for (int s = wide >> 1; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+        float x[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+        if (ok) {
+          for (int i = c0 + sub; i <= c1; i += wide) {
+            const float* p = slot_of(i, c1);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
+            const float f = rescale(__ldcg(p + R * D + row), m);
+            x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]);
+            x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+            x[4] = fmaf(f, __ldcg(p + R * D + R + row), x[4]);
+          }
         }
-        finish<D, DT, R>(a, seq, tile, kvh, row, e - row * D, x, l);
+        for (int s = wide >> 1; s; s >>= 1)
+#pragma unroll
+          for (int k = 0; k < 5; ++k) x[k] += __shfl_xor_sync(0xFFFFFFFFu, x[k], s);
+        if (ok && sub == 0) {
+          size_t at;
+          out_row<D, R>(a, seq, tile, kvh, row, at);
+          const float f = inverse(a, x[4]);
+          const float y[4] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f};
+          store_out<DT, 4>(a.out, at + e * 4 - row * D, y);
+        }
       }
     }
   }
   if (!a.accumulate) return;
 
-  long long v = v0;
-  int seq = v < v1 ? f_seq[1] : 0;
-  long long start = v < v1 ? f_start[1] : 0;   // in units of all row tiles
-  while (v < v1) {
-    int n = a.c.len(seq);
+  // Units of all row tiles share their keys: the line without row tiles, in
+  // equal ranges of one CTA each.
+  const int keys_total = line.total / a.tiles;
+  int v = (int)((long long)keys_total * blockIdx.x / gridDim.x);
+  const int v_end = (int)((long long)keys_total * (blockIdx.x + 1) / gridDim.x);
+  if (v >= v_end) return;
+  int seq, start;   // start: in units of all row tiles
+  line_find(a, scan, v * a.tiles, seq, start);
+  int n = a.c.len(seq);
+  while (v < v_end) {
     while (n == 0) n = a.c.len(++seq);
-    const int nb = blocks_of(n);
-    const long long in_seq = v - start / a.tiles;
-    const int kvh = (int)(in_seq / nb), b0 = (int)(in_seq - (long long)kvh * nb);
-    const int b1 = (int)(v1 - v < nb - b0 ? b0 + (v1 - v) : nb);
-    // each row's maximum and the reciprocal of its sum, one warp a row
-    __syncthreads();
-    for (int row = warp; row < a.tiles * R; row += kThreadsM / 32) {
-      const int tile = row / R, rr = row - tile * R;
-      const int item = tile * a.c.heads + kvh;
-      const long long i0 = start + (long long)item * nb;
-      const int c0 = cta_of(i0), c1 = cta_of(i0 + nb - 1);
-      float m = -INFINITY, l = 0.f;
-      if (c0 == c1) {
-        const float* p = a.stats + (((size_t)seq * per_item + item) * R + rr) * 2;
-        m = __ldcg(p); l = __ldcg(p + 1);
-      } else {
-        for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, __ldcg(slot_of(i, c1) + R * D + rr));
+    const int nb = blocks_of(n), in_seq = v - start / a.tiles;
+    const int kvh = in_seq / (nb + kStart), head_at = start / a.tiles + kvh * (nb + kStart);
+    const int stop = min(v_end, head_at + nb + kStart);
+    const int b0 = max(v - head_at - kStart, 0), b1 = stop - head_at - kStart;
+    if (b1 > b0) {
+      // each row's maximum and the reciprocal of its sum, one warp a row
+      __syncthreads();
+      for (int row = warp; row < a.rows; row += kWarpsM) {
+        const int tile = row / R, rr = row - tile * R, item = tile * a.c.heads + kvh;
+        const int i0 = start + item * (nb + kStart) + kStart;
+        const int c0 = line.cta_of(i0), c1 = line.cta_of(i0 + nb - 1);
+        float m = -INFINITY, l = 0.f;
+        if (c0 == c1) {
+          const float2 st = __ldcg(reinterpret_cast<const float2*>(a.stats) + ((size_t)seq * items + item) * R + rr);
+          m = st.x; l = st.y;
+        } else {
+          for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, __ldcg(slot_of(i, c1) + R * D + rr));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        for (int i = c0 + lane; i <= c1; i += 32) {
-          const float* p = slot_of(i, c1);
-          const float mi = __ldcg(p + R * D + rr);
-          l += (mi == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mi - m)) * __ldcg(p + R * D + R + rr);
+          for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+          for (int i = c0 + lane; i <= c1; i += 32) {
+            const float* p = slot_of(i, c1) + R * D + rr;
+            l = fmaf(rescale(__ldcg(p), m), __ldcg(p + R), l);
+          }
+#pragma unroll
+          for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        // sums carry the bias of the probabilities
+        if (lane == 0) stat[row] = make_float2(m == -INFINITY ? 0.f : kBias - m, l != 0.f ? 1.f / l : 0.f);
       }
-      // sums carry the bias of the probabilities; rows behind the last add nothing
-      if (lane == 0 && row < kMaxRows) {
-        stat_m[row] = m == -INFINITY ? 0.f : m - kBias;
-        stat_l[row] = row < a.rows && l != 0.f ? 1.f / l : 0.f;
+      __syncthreads();
+      float* score = a.c.scores + ((size_t)seq * a.c.heads + kvh) * a.c.capacity();
+      for (int key = b0 * kKv4Block + tid; key < min(n, b1 * kKv4Block); key += kThreadsM) {
+        const float old = __ldcg(score + key);
+        float w = 0.f;
+        for (int tile = 0; tile < a.tiles; ++tile) {
+          const int unit = start + (tile * a.c.heads + kvh) * (nb + kStart) + kStart + key / kKv4Block;
+          const float* s = a.s_all + ((size_t)unit * kKv4Block + key % kKv4Block) * a.s_rows;
+#pragma unroll 4
+          for (int i = 0; i < a.s_rows; i += 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(s + i));
+            const int row = tile * R + i;
+            if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
+            if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
+          }
+        }
+        score[key] = old + w;
       }
     }
-    __syncthreads();
-    float* score = a.c.scores + ((size_t)seq * a.c.heads + kvh) * a.c.capacity();
-    for (int key = b0 * kKv4Block + tid; key < min(n, b1 * kKv4Block); key += kThreadsM) {
-      float w = 0.f;
-      for (int tile = 0; tile < a.tiles; ++tile) {
-        const long long unit = start + (long long)(tile * a.c.heads + kvh) * nb + key / kKv4Block;
-        const float* s = a.s_all + ((size_t)unit * kKv4Block + key % kKv4Block) * a.s_rows;
-        for (int i = 0; i < a.s_rows; i += 2) {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(s + i));
-          const int row = tile * R + i;
-          if (row < a.rows) w += ex2(x.x - stat_m[row]) * stat_l[row];
-          if (row + 1 < a.rows) w += ex2(x.y - stat_m[row + 1]) * stat_l[row + 1];
-        }
-      }
-      score[key] = __ldcg(score + key) + w;
-    }
-    v += b1 - b0;
+    v = stop;
     if (b1 == nb && kvh + 1 == a.c.heads) {
-      start += (long long)nb * per_item;
+      start += (nb + kStart) * items;
       ++seq;
+      n = v < v_end ? a.c.len(seq) : 0;
     }
   }
 }
@@ -860,8 +904,8 @@ Layout layout_of(const mk_kv4_cache* c, int q_len, int group, bool accumulate) {
     const size_t items = (size_t)c->n_seq * l.tiles * c->n_kv_heads;
     at = up(at + items * l.R * 2 * sizeof(float));
     l.s_all = at;
-    const size_t blocks = ((size_t)c->pages_per_seq * c->page_tokens + kKv4Block - 1) / kKv4Block;
-    at = up(at + items * blocks * kKv4Block * l.s_rows * sizeof(float));
+    const size_t units = (size_t)c->pages_per_seq * c->page_tokens / kKv4Block + kStart;
+    at = up(at + items * units * kKv4Block * l.s_rows * sizeof(float));
   }
   l.bytes = at;
   return l;
@@ -873,6 +917,10 @@ int check_shape(const mk_kv4_cache* c, int q_len, int n_q_heads, const char* who
     return kv4_fail(MK_ERR_INVALID_ARG, who, "n_q_heads is a multiple of n_kv_heads");
   if (q_len < 1 || (long long)q_len * (n_q_heads / c->n_kv_heads) > kMaxRows)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "q_len times the query heads of a KV head is 1 to 1024");
+  const long long rows = (long long)q_len * (n_q_heads / c->n_kv_heads);
+  const double units = ((double)c->pages_per_seq * c->page_tokens / kKv4Block + kStart) * c->n_seq * c->n_kv_heads *
+                       (double)(rows <= 8 ? 1 : (rows + 15) / 16);
+  if (units > 2147483000.0) return kv4_fail(MK_ERR_UNSUPPORTED, who, "more than 2^31 blocks of keys and rows in one call");
   return MK_OK;
 }
 
@@ -924,8 +972,8 @@ extern "C" int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, in
   if (q_stride < (long long)n_q_heads * cache->head_dim || q_stride > (1ll << 40))
     return kv4_fail(MK_ERR_INVALID_ARG, who, "a token's stride is at least n_q_heads * head_dim");
   if ((reinterpret_cast<uintptr_t>(q_dev) & 15u) || (q_stride * esz) % 16 ||
-      (reinterpret_cast<uintptr_t>(out_dev) & (esz - 1)))
-    return kv4_fail(MK_ERR_INVALID_ARG, who, "queries of a token are 16-byte aligned, outputs to their type");
+      (reinterpret_cast<uintptr_t>(out_dev) & 15u))
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "queries of a token and the outputs are 16-byte aligned");
   if (!(scale > 0.f) || !(scale <= 3.0e38f)) return kv4_fail(MK_ERR_INVALID_ARG, who, "scale is positive and finite");
   if (accumulate && !cache->scores_dev)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "weights are added to a cache's scores, and this one has none");

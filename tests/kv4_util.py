@@ -104,11 +104,12 @@ class Plain:
                                                   + rng.integers(0, 8, b[..., BLOCK * self.dim // 2:].shape))
 
 
-# A probability enters the products as fp16, 2^15 at the row's maximum: below
-# 2^-29 of it the type's step is fixed, 2^-24 / 2^15 = 2^-39 of the maximum, and the
-# rounding half of that, however small the probability.  In units of the smallest
-# relative error that a bound multiplies the mass with (2^-18, _bound): 2^-22.
-TINY = 2.0 ** -22
+# A probability enters the products as fp16, 2^11 to 2^15 at the row's maximum:
+# far below it the type's step is fixed, 2^-24 / 2^11 = 2^-35 of the maximum at
+# most, and the rounding half of that, however small the probability.  In units
+# of the smallest relative error that a bound multiplies the mass with (2^-18,
+# _bound): 2^-18.
+TINY = 2.0 ** -18
 
 
 def attend(q, k, v, scale, group):
