@@ -11,6 +11,8 @@ import ctypes as C
 import os
 from typing import Dict, List, Optional, Sequence
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 # MK_LIBRARY selects another build of the library (A/B comparisons of builds).
 LIB_PATH = os.environ.get("MK_LIBRARY") or os.path.join(HERE, "libmk.so")
@@ -241,7 +243,6 @@ def prefill_graph(model, T: int, tiles, lm_req, num_ctas: int):
 
 class Plan:
     """The task graph mk_create would build (host only)."""
-
     def __init__(self, model, max_seq: int, num_ctas: int, max_batch: int = 1,
                  attn_splits: int = 0, weight_format: int = 0):
         L = lib()
@@ -291,14 +292,12 @@ def qkv_row_source(model, r: int):
 class Decoder:
     """One libmk context.  ``weights`` maps the synthetic generator's names to
     CUDA bf16 tensors; mk_create copies them, so they may be dropped after."""
-
     def __init__(self, model, weights: Dict[str, "torch.Tensor"], max_seq: int,
                  max_batch: int = 1, num_ctas: int = 0, attn_splits: int = 0,
                  timeout_ms: int = 0, mode: int = MODE_MEGAKERNEL, stream=None,
                  l2_prefetch: int = 0, prefill_steps: int = 0, batch_sequential: int = 0,
                  weight_format: int = 0, kv_page_tokens: int = 0, kv_pool_pages: int = 0,
                  prefill_per_operator: int = 0, prefill_attention: int = 0):
-        import torch
         L = lib()
         self.model = model
         self.max_seq = max_seq
@@ -392,7 +391,6 @@ class Decoder:
         """Positions [first, n_pos) of slot slots[b] (slot b without ``slots``)
         become those of slot slots[parents_dev[b]], in place (see
         mk_kv_reorder); ``parents_dev`` int32 CUDA, one entry per slot."""
-        import torch
         _tensor(parents_dev, torch.int32, "parents_dev")
         n = parents_dev.numel() if slots is None else len(slots)
         if n != parents_dev.numel():
@@ -407,7 +405,6 @@ class Decoder:
         go on with it.  Uses slots 0..beams-1; after the prefill, steps,
         selection and the caches' reordering are enqueued without a host round
         trip."""
-        import torch
         if not 1 <= beams <= self.max_batch:
             raise ValueError("beams is 1 to max_batch")
         n, V, dev = prompt_dev.numel(), self.model.vocab, prompt_dev.device
@@ -502,7 +499,6 @@ class Decoder:
 
 def read_probe(src_dev, sink_dev, stream=None):
     """Enqueues one read-only pass over ``src_dev`` (a contiguous CUDA tensor)."""
-    import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     nbytes = src_dev.numel() * src_dev.element_size()
     _check(lib().mk_read_probe(src_dev.data_ptr(), nbytes, sink_dev.data_ptr(), st.cuda_stream))
@@ -515,7 +511,6 @@ def attention_workspace_bytes(n_q_per_kv: int, head_dim: int, splits: int) -> in
 def attention_decode(q_dev, k_dev, v_dev, n_keys: int, splits: int, workspace_dev, out_dev,
                      stream=None):
     """Split-KV decode attention for one KV head (see mk_attention_decode)."""
-    import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     G, d = q_dev.shape
     _check(lib().mk_attention_decode(q_dev.data_ptr(), k_dev.data_ptr(), v_dev.data_ptr(),
@@ -527,7 +522,6 @@ def attention_decode_noalloc(q_dev, k_dev, v_dev, n_keys: int, splits: int, out_
                              stream=None):
     """mk_attention_decode with the library's static scratch instead of a
     caller workspace (see mk_attention_decode_noalloc)."""
-    import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     G, d = q_dev.shape
     _check(lib().mk_attention_decode_noalloc(q_dev.data_ptr(), k_dev.data_ptr(),
@@ -537,39 +531,40 @@ def attention_decode_noalloc(q_dev, k_dev, v_dev, n_keys: int, splits: int, out_
 
 # ------------------------------------- the state of a decode: 4-bit cache, beams
 
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_FLAGS = (torch.bool, torch.uint8)
+
+
 def _dtype(t) -> int:
-    import torch
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"fp32, bf16 or fp16 expected, got {t.dtype}")
     return code
 
 
-def _tensor(t, dtype, what, shape=None):
-    if not t.is_cuda or (dtype is not None and t.dtype != dtype) or not t.is_contiguous():
+def _tensor(t, dtype, what, shape=None, device=None):
+    """Pointer of a contiguous CUDA tensor, its type, shape and device (index) checked."""
+    d = t.get_device()
+    if d < 0 or (dtype is not None and t.dtype != dtype) or not t.is_contiguous():
         raise TypeError(f"{what}: a contiguous CUDA tensor{'' if dtype is None else f' of {dtype}'} expected")
+    if device is not None and d != device:
+        raise ValueError(f"{what}: on device {d}, the others on {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _on(device, stream, call, *args):
-    """Runs ``call(*args, stream)`` on the tensors' device; the stream is
-    ``stream``, or that device's current one."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        _check(call(*args, stream.cuda_stream))
+    """Runs ``call(*args, stream)`` with the tensors' device (index) current; the
+    stream is ``stream``, or that device's current one."""
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        rc = call(*args, raw)
     else:
         with torch.cuda.device(device):
-            _check(call(*args, stream.cuda_stream))
-
-
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors on one device: {t.device} and {device}")
+            rc = call(*args, raw)
+    if rc:
+        _check(rc)
 
 
 def kv4_page_bytes(n_kv_heads: int, head_dim: int, page_tokens: int) -> int:
@@ -583,12 +578,9 @@ class Kv4Cache:
     ``scores`` fp32 [n_seq, n_kv_heads, pages_per_seq * page_tokens] or None.
     Holds the tensors, copies nothing; their contents may change between
     calls, their storage not."""
-
     def __init__(self, pool, lens, n_kv_heads: int, head_dim: int, page_tokens: int, table=None,
                  scores=None, k_log2: int = 0, v_log2: int = 0):
-        import torch
-        L = lib()
-        page = L.mk_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
+        page = lib().mk_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
         if page == 0:
             raise MkError(-9, "head_dim is 64 or 128, page_tokens a multiple of 32")
         if pool.dim() != 2 or lens.dim() != 1 or pool.shape[1] != page:
@@ -605,22 +597,21 @@ class Kv4Cache:
         self.capacity = per * page_tokens
         self.n_kv_heads, self.head_dim, self.page_tokens = n_kv_heads, head_dim, page_tokens
         self.pool, self.lens, self.table, self.scores = pool, lens, table, scores
-        self.device = pool.device
-        _same_device(self.device, lens, table, scores)
+        self.device = d = pool.get_device()
         self.c = Kv4Struct(n_kv_heads, head_dim, page_tokens, pool.shape[0], self.n_seq, per, k_log2,
                            v_log2, _tensor(pool, torch.uint8, "pool"),
-                           None if table is None else _tensor(table, torch.int32, "table"),
-                           _tensor(lens, torch.int32, "lens"),
+                           None if table is None else _tensor(table, torch.int32, "table", None, d),
+                           _tensor(lens, torch.int32, "lens", None, d),
                            None if scores is None else _tensor(
-                               scores, torch.float32, "scores", (self.n_seq, n_kv_heads, self.capacity)))
+                               scores, torch.float32, "scores", (self.n_seq, n_kv_heads, self.capacity), d))
         self.ref = C.addressof(self.c)
 
 
-def _rows(t, heads, dim, what):
-    """(pointer, elements between tokens) of token rows [..., heads, dim] whose
-    heads lie together."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: CUDA [tokens, {heads}, {dim}] expected, got {tuple(t.shape)}")
+def _rows(t, heads, dim, what, device):
+    """(pointer, elements between tokens) of token rows [tokens, heads, dim]
+    whose heads lie together."""
+    if t.get_device() != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what}: [tokens, {heads}, {dim}] on the cache's device expected, got {tuple(t.shape)}")
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{what}: a token's heads and dims are contiguous")
@@ -631,24 +622,25 @@ def kv4_append(cache: Kv4Cache, k, v, offsets, stream=None):
     """Packed new tokens k, v [tokens, n_kv_heads, head_dim] (token rows may be
     strided) into the cache; tokens offsets[s]..offsets[s+1] are the newest of
     sequence s, which cache.lens counts already (see mk_kv4_append)."""
-    import torch
-    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k")
-    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v")
-    if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
+    d = cache.device
+    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k", d)
+    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v", d)
+    n = k.shape[0]
+    if n != v.shape[0] or k.dtype != v.dtype:
         raise ValueError("k and v have the same tokens and type")
-    _same_device(cache.device, k, v, offsets)
-    _on(cache.device, stream, lib().mk_kv4_append, cache.ref, kp, vp, _dtype(k), ks, vs,
-        _tensor(offsets, torch.int32, "offsets", (cache.n_seq + 1,)), k.shape[0])
+    _on(d, stream, lib().mk_kv4_append, cache.ref, kp, vp, _dtype(k), ks, vs,
+        _tensor(offsets, torch.int32, "offsets", (cache.n_seq + 1,), d), n)
 
 
 def kv4_read(cache: Kv4Cache, k_out, v_out, stream=None):
     """Values of slots [0, min(n, lens)) into k_out, v_out [n_seq, n,
     n_kv_heads, head_dim]; other rows are left (see mk_kv4_read)."""
-    n = k_out.shape[1]
+    if k_out.dim() != 4:
+        raise ValueError("k_out is [n_seq, n, n_kv_heads, head_dim]")
+    n, d = k_out.shape[1], cache.device
     shape = (cache.n_seq, n, cache.n_kv_heads, cache.head_dim)
-    _same_device(cache.device, k_out, v_out)
-    _on(cache.device, stream, lib().mk_kv4_read, cache.ref, _dtype(k_out), n,
-        _tensor(k_out, None, "k_out", shape), _tensor(v_out, k_out.dtype, "v_out", shape))
+    _on(d, stream, lib().mk_kv4_read, cache.ref, _dtype(k_out), n, _tensor(k_out, None, "k_out", shape, d),
+        _tensor(v_out, k_out.dtype, "v_out", shape, d))
 
 
 def attention_kv4_workspace_bytes(cache: Kv4Cache, q_len: int, n_q_heads: int,
@@ -662,17 +654,21 @@ def attention_kv4(cache: Kv4Cache, q, out, workspace, scale: Optional[float] = N
     [n_seq, q_len, n_q_heads, head_dim], over the cache; ``scale`` is
     1/sqrt(head_dim) unless given, ``accumulate`` adds the weights to
     cache.scores (see mk_attention_kv4)."""
-    if q.dim() != 4 or q.shape[0] != cache.n_seq or q.shape[3] != cache.head_dim:
-        raise ValueError(f"q: [{cache.n_seq}, q_len, n_q_heads, {cache.head_dim}] expected, got {tuple(q.shape)}")
-    n_seq, q_len, heads, dim = q.shape
-    st = q.stride()
-    row = st[1] if q_len > 1 else (st[0] if n_seq > 1 else heads * dim)
-    if not q.is_cuda or st[3] != 1 or (heads > 1 and st[2] != dim) or (n_seq > 1 and st[0] != q_len * row):
-        raise ValueError("q: a token's heads and dims are contiguous, tokens evenly spaced")
-    _same_device(cache.device, q, out, workspace)
-    _on(cache.device, stream, lib().mk_attention_kv4, cache.ref, q.data_ptr(), _dtype(q), q_len, heads, row,
-        dim ** -0.5 if scale is None else scale, int(accumulate), _tensor(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _tensor(out, q.dtype, "out", q.shape))
+    shape, d = q.shape, cache.device
+    if len(shape) != 4 or shape[0] != cache.n_seq or shape[3] != cache.head_dim or q.get_device() != d:
+        raise ValueError(f"q: [{cache.n_seq}, q_len, n_q_heads, {cache.head_dim}] on the cache's device "
+                         f"expected, got {tuple(shape)}")
+    n_seq, q_len, heads, dim = shape
+    if q.is_contiguous():
+        row = heads * dim
+    else:
+        st = q.stride()
+        row = st[1] if q_len > 1 else (st[0] if n_seq > 1 else heads * dim)
+        if st[3] != 1 or (heads > 1 and st[2] != dim) or (n_seq > 1 and st[0] != q_len * row):
+            raise ValueError("q: a token's heads and dims are contiguous, tokens evenly spaced")
+    _on(d, stream, lib().mk_attention_kv4, cache.ref, q.data_ptr(), _dtype(q), q_len, heads, row,
+        dim ** -0.5 if scale is None else scale, accumulate, _tensor(workspace, None, "workspace", None, d),
+        workspace.nbytes, _tensor(out, q.dtype, "out", shape, d))
 
 
 def kv4_evict(src: Kv4Cache, dst: Kv4Cache, budget: int, keep_first: int, keep_last: int, kept,
@@ -680,20 +676,20 @@ def kv4_evict(src: Kv4Cache, dst: Kv4Cache, budget: int, keep_first: int, keep_l
     """The rows of src that a budget leaves -- its ends and the highest scores
     -- into dst, their slots into kept int32 [n_seq, n_kv_heads, budget] (see
     mk_kv4_evict)."""
-    import torch
-    _same_device(src.device, dst.pool, kept)
-    _on(src.device, stream, lib().mk_kv4_evict, src.ref, dst.ref, budget, keep_first, keep_last,
-        _tensor(kept, torch.int32, "kept", (src.n_seq, src.n_kv_heads, budget)))
+    d = src.device
+    if dst.device != d:
+        raise ValueError(f"caches on devices {d} and {dst.device}")
+    _on(d, stream, lib().mk_kv4_evict, src.ref, dst.ref, budget, keep_first, keep_last,
+        _tensor(kept, torch.int32, "kept", (src.n_seq, src.n_kv_heads, budget), d))
 
 
 def kv4_reorder(cache: Kv4Cache, parents, first: int, n_keys: int, stream=None):
     """Reorders the sequences of each search in place: parents int32
     [n_seq / beams, beams] (see mk_kv4_reorder)."""
-    import torch
     if parents.dim() != 2 or parents.numel() != cache.n_seq:
         raise ValueError("parents is [searches, beams], one entry per sequence")
-    _same_device(cache.device, parents)
-    _on(cache.device, stream, lib().mk_kv4_reorder, cache.ref, _tensor(parents, torch.int32, "parents"),
+    d = cache.device
+    _on(d, stream, lib().mk_kv4_reorder, cache.ref, _tensor(parents, torch.int32, "parents", None, d),
         parents.shape[1], first, n_keys)
 
 
@@ -707,23 +703,23 @@ def beam_select(logits, cum, tokens, parents, scores, workspace, finished=None, 
     be strided), cum fp32 [n_batch, beams] -> tokens, parents int32, scores
     fp32 and finished_out (bool or uint8), all [n_batch, beams] (see
     mk_beam_select)."""
-    import torch
-    shape = cum.shape
+    shape, d = cum.shape, logits.get_device()
     if len(shape) != 2 or logits.dim() != 2 or logits.shape[0] != shape[0] * shape[1]:
         raise ValueError("cum is [n_batch, beams], logits [n_batch * beams, vocab]")
-    if not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    rows, vocab = logits.shape
+    st = logits.stride()
+    if d < 0 or (vocab > 1 and st[1] != 1):
         raise ValueError("logits: CUDA, contiguous rows")
-    for f in (finished, finished_out):
-        if f is not None and f.dtype not in (torch.bool, torch.uint8):
-            raise TypeError("finished flags are bool or uint8")
-    _same_device(logits.device, cum, tokens, parents, scores, workspace, finished, finished_out)
-    _on(logits.device, stream, lib().mk_beam_select, logits.data_ptr(), _dtype(logits),
-        logits.stride(0) if logits.shape[0] > 1 else logits.shape[1], _tensor(cum, torch.float32, "cum"),
-        None if finished is None else _tensor(finished, None, "finished", shape), shape[0], shape[1],
-        logits.shape[1], eos, _tensor(tokens, torch.int32, "tokens", shape),
-        _tensor(parents, torch.int32, "parents", shape), _tensor(scores, torch.float32, "scores", shape),
-        None if finished_out is None else _tensor(finished_out, None, "finished_out", shape),
-        _tensor(workspace, None, "workspace"), workspace.numel() * workspace.element_size())
+    if (finished is not None and finished.dtype not in _FLAGS) or \
+            (finished_out is not None and finished_out.dtype not in _FLAGS):
+        raise TypeError("finished flags are bool or uint8")
+    _on(d, stream, lib().mk_beam_select, logits.data_ptr(), _dtype(logits), st[0] if rows > 1 else vocab,
+        _tensor(cum, torch.float32, "cum", None, d),
+        None if finished is None else _tensor(finished, None, "finished", shape, d), shape[0], shape[1],
+        vocab, eos, _tensor(tokens, torch.int32, "tokens", shape, d),
+        _tensor(parents, torch.int32, "parents", shape, d), _tensor(scores, torch.float32, "scores", shape, d),
+        None if finished_out is None else _tensor(finished_out, None, "finished_out", shape, d),
+        _tensor(workspace, None, "workspace", None, d), workspace.nbytes)
 
 
 def beam_reorder(state, parents, first: int, count: int, stream=None):
@@ -731,17 +727,14 @@ def beam_reorder(state, parents, first: int, count: int, stream=None):
     any type) in place by parents int32 [n_batch, beams]; positions [first,
     first + count) of every segment move, the others stay (see
     mk_beam_reorder)."""
-    import torch
-    base = _tensor(state, None, "state")
+    base, d = _tensor(state, None, "state"), state.get_device()
     if state.dim() < 3 or parents.dim() != 2 or parents.numel() != state.shape[0]:
         raise ValueError("state is [n_batch * beams, segments, positions, ...], parents [n_batch, beams]")
     segments, positions = state.shape[1], state.shape[2]
     if first < 0 or count < 0 or first + count > positions:
         raise ValueError("positions [first, first + count) of the state")
-    if state.numel() == 0 or count == 0:
+    if count == 0 or state.numel() == 0:
         return
     row = state.element_size() * state.stride(2)
-    _same_device(state.device, parents)
-    _on(state.device, stream, lib().mk_beam_reorder, base + first * row,
-        _tensor(parents, torch.int32, "parents"), parents.shape[0], parents.shape[1],
-        segments * positions * row, segments, positions * row, count * row)
+    _on(d, stream, lib().mk_beam_reorder, base + first * row, _tensor(parents, torch.int32, "parents", None, d),
+        parents.shape[0], parents.shape[1], segments * positions * row, segments, positions * row, count * row)

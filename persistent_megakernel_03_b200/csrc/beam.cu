@@ -16,11 +16,16 @@ namespace {
 // the W highest are wanted.  Inside a beam the order is that of the logits, so
 // no score is needed to find a beam's own W best: the vocabulary is read once,
 // in chunks of 4,096 that stay in registers, and each chunk gives its W
-// highest logits, its maximum and its sum of exponentials.  A second kernel,
-// one CTA a search and one warp a beam, joins the chunks: the log-sum-exp, the
-// beam's W best (they lie in the W chunks with the highest heads), then the
-// best of W * W scores.  Scores are compared in 64 bits, so that candidates of
-// different beams are not ordered by rounding.
+// highest logits, its maximum and its sum of exponentials.  The W-th highest
+// maximum of the chunk's 32 groups of 8 threads bounds the W-th highest logit
+// from below, so only logits from that bound on are looked at again, a few
+// more than W (taking W rounds of maxima over all logits of a warp instead
+// took twice the time: 16 x 4 rows of 151,936 in bf16 27 us).  Where
+// ties make them too many, rounds over all logits find the lowest places.  A
+// second kernel, one CTA a search and one warp a beam, joins the chunks: the
+// log-sum-exp, the beam's W best (they lie in the W chunks with the highest
+// heads), then the best of W * W scores.  Scores are compared in 64 bits, so
+// that candidates of different beams are not ordered by rounding.
 //
 // Bound: the logits' bytes once (4.1 MB for 8 beams of 128,256 in fp32: under
 // 1 us) beside two launches and W rounds of warp maxima in each.
@@ -30,8 +35,9 @@ constexpr int kWarpsS = kThreadsS / 32;
 constexpr int kPer = 16;                        // logits of a thread
 constexpr int kChunk = kThreadsS * kPer;
 constexpr int kMaxBeams = 16;
+constexpr int kFound = 128;                     // logits from the bound on that a chunk keeps
+static_assert(kWarpsS * 4 == 32, "a group's maximum for every lane");
 constexpr int kMaxChunks = 256;                 // vocabulary up to 1,048,576
-constexpr int kHeads = kMaxChunks / 32;         // chunk heads of a lane
 
 // fp32 to an integer of the same order; 0 for what is no candidate (-inf, NaN).
 __device__ __forceinline__ uint32_t logit_key(float f) {
@@ -42,6 +48,12 @@ __device__ __forceinline__ uint32_t logit_key(float f) {
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The lane whose (key, index) is first: highest key, then lowest index.
@@ -66,9 +78,9 @@ struct SelectArgs {
 };
 
 __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs a) {
-  __shared__ uint2 best[kWarpsS][kMaxBeams];
-  __shared__ uint32_t tops[kWarpsS];
-  __shared__ float parts[kWarpsS];
+  __shared__ uint2 best[kWarpsS][kMaxBeams], list[kFound];
+  __shared__ float tops[32], parts[kWarpsS];
+  __shared__ int found;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = a.beams;
@@ -131,6 +143,76 @@ __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs 
     }
   }
 
+  // maxima of the threads (fmaxf passes NaN by), the groups, the chunk
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+  float group = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  group = fmaxf(group, __shfl_xor_sync(0xFFFFFFFFu, group, 2));
+  group = fmaxf(group, __shfl_xor_sync(0xFFFFFFFFu, group, 4));
+  if ((lane & 7) == 0) tops[warp * 4 + (lane >> 3)] = group;
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
+  uint32_t left = logit_key(tops[lane]);   // a group a lane
+  const uint32_t highest = __reduce_max_sync(0xFFFFFFFFu, left);
+  const float mx = highest ? key_logit(highest) : 0.f;
+  uint32_t bound = highest;
+  for (int j = 0; j < W; ++j) {
+    bound = __reduce_max_sync(0xFFFFFFFFu, left);
+    if (bound == 0u) break;   // fewer groups with a candidate: look at every one
+    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0u;
+  }
+  // the W-th highest maximum, or everything
+  const float least = bound ? key_logit(bound) : -INFINITY;
+  if (top >= least && top > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (x[i] >= least && x[i] > -INFINITY) {
+        const int to = atomicAdd(&found, 1);   // any order: places decide below
+        if (to < kFound) list[to] = make_uint2(logit_key(x[i]), at(i));
+      }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sum += ex2((x[i] - mx) * 1.44269504f);   // -inf adds 0, NaN goes through
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) parts[warp] = sum;
+  __syncthreads();
+  const size_t chunk = row * a.chunks + blockIdx.x;
+  uint2* out = a.lists + chunk * W;
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarpsS; ++w) s += parts[w];
+    a.sums[chunk] = make_float2(highest ? mx : -INFINITY, s);
+  }
+  if (found <= kFound) {
+    if (warp) return;
+    // each lane's share of the list, then W rounds
+    uint2 mine[kFound / 32];
+#pragma unroll
+    for (int i = 0; i < kFound / 32; ++i) {
+      mine[i] = make_uint2(0u, 0u);
+      if (i * 32 + lane < found) mine[i] = list[i * 32 + lane];
+    }
+    for (int j = 0; j < W; ++j) {
+      uint2 b = mine[0];
+#pragma unroll
+      for (int i = 1; i < kFound / 32; ++i)
+        if (mine[i].x > b.x || (mine[i].x == b.x && mine[i].y < b.y)) b = mine[i];
+      uint32_t k, i0;
+      warp_first(b.x, b.y, k, i0);
+      if (lane == 0) out[j] = make_uint2(k, k ? i0 : 0u);
+#pragma unroll
+      for (int i = 0; i < kFound / 32; ++i)
+        if (mine[i].x == k && mine[i].y == i0) mine[i].x = 0u;
+    }
+    return;
+  }
+
+  // more logits on the bound than the list holds: rounds of maxima, a warp's W
+  // highest first, then those of the warps
   uint32_t key[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) key[i] = logit_key(x[i]);
@@ -142,9 +224,6 @@ __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs 
       if (key[i] > mine) { mine = key[i]; which = i; }   // at() grows with i
   };
   rescan();
-  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, mine);
-  if (lane == 0) tops[warp] = top;
-  // this warp's W highest
   for (int j = 0; j < W; ++j) {
     uint32_t k, i;
     warp_first(mine, at(which), k, i);
@@ -161,27 +240,8 @@ __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs 
     }
   }
   __syncthreads();
-  uint32_t m = 0;
-#pragma unroll
-  for (int w = 0; w < kWarpsS; ++w) m = max(m, tops[w]);
-  const float mx = m ? key_logit(m) : 0.f;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) sum += exp2f((x[i] - mx) * 1.44269504f);   // -inf adds 0, NaN goes through
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) parts[warp] = sum;
-  __syncthreads();
   if (warp) return;
-  const size_t chunk = row * a.chunks + blockIdx.x;
-  if (lane == 0) {
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarpsS; ++w) s += parts[w];
-    a.sums[chunk] = make_float2(m ? mx : -INFINITY, s);
-  }
-  // join of the warps' lists: lane l (of kWarpsS) walks list l
-  uint2* out = a.lists + chunk * W;
+  // lane l (of kWarpsS) walks list l
   int head = 0;
   uint2 h = lane < kWarpsS ? best[lane][0] : make_uint2(0u, 0u);
   for (int j = 0; j < W; ++j) {
@@ -203,12 +263,13 @@ __device__ __forceinline__ unsigned long long score_key64(double s) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-constexpr int kFinal = kMaxBeams * kMaxBeams / 32;   // candidates of a lane
-
-__global__ void __launch_bounds__(kMaxBeams * 32) beam_join_kernel(const SelectArgs a) {
-  __shared__ unsigned long long cand_key[kMaxBeams * kMaxBeams];
-  __shared__ double cand_score[kMaxBeams * kMaxBeams];
-  __shared__ int32_t cand_token[kMaxBeams * kMaxBeams];
+// HEADS: chunk heads of a lane.  WT: most beams; WT * WT / 32 candidates a lane.
+template <int HEADS, int WT>
+__global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) {
+  constexpr int kFinal = WT * WT < 32 ? 1 : WT * WT / 32;
+  __shared__ unsigned long long cand_key[WT * WT];
+  __shared__ double cand_score[WT * WT];
+  __shared__ int32_t cand_token[WT * WT];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5, W = a.beams;
@@ -240,9 +301,9 @@ __global__ void __launch_bounds__(kMaxBeams * 32) beam_join_kernel(const SelectA
     const double lse = (double)mx + log(sum);
     // the W chunks with the highest heads
     const uint2* lists = a.lists + row * a.chunks * W;
-    uint2 head[kHeads];
+    uint2 head[HEADS];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < HEADS; ++i) {
       const int c = i * 32 + lane;
       head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
     }
@@ -250,14 +311,14 @@ __global__ void __launch_bounds__(kMaxBeams * 32) beam_join_kernel(const SelectA
     for (int j = 0; j < W; ++j) {
       uint32_t mine = 0, tok = 0xFFFFFFFFu;
 #pragma unroll
-      for (int i = 0; i < kHeads; ++i)
+      for (int i = 0; i < HEADS; ++i)
         if (head[i].x > mine) { mine = head[i].x; tok = head[i].y; }   // chunks grow with i
       uint32_t k, t;
       warp_first(mine, tok, k, t);
       if (k == 0u) break;
       if (lane == j) chosen = (int)t / kChunk;
 #pragma unroll
-      for (int i = 0; i < kHeads; ++i)
+      for (int i = 0; i < HEADS; ++i)
         if (head[i].x == k && head[i].y == t) head[i].x = 0u;
     }
     // their lists: W * W keys, a lane's share in registers
@@ -455,7 +516,10 @@ extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_s
   a.lists = reinterpret_cast<uint2*>(a.sums + rows * a.chunks);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = pdl_launch(beam_chunk_kernel, dim3(a.chunks, (unsigned)rows), dim3(kThreadsS), 0, st, a);
-  if (e == cudaSuccess) e = pdl_launch(beam_join_kernel, dim3(n_batch), dim3(32 * beams), 0, st, a);
+  auto join = beams <= 4 ? (a.chunks <= 64 ? beam_join_kernel<2, 4> : beam_join_kernel<8, 4>)
+              : beams <= 8 ? (a.chunks <= 64 ? beam_join_kernel<2, 8> : beam_join_kernel<8, 8>)
+                           : (a.chunks <= 64 ? beam_join_kernel<2, 16> : beam_join_kernel<8, 16>);
+  if (e == cudaSuccess) e = pdl_launch(join, dim3(n_batch), dim3(32 * beams), 0, st, a);
   return e == cudaSuccess ? MK_OK : fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
 }
 

@@ -85,54 +85,70 @@ __device__ __forceinline__ void load16(const void* p, int dtype, float (&x)[16])
 
 // One group: the scale is e4m3(max |x| / 6), rounded to nearest even and at
 // most 448; a code is the e2m1 value nearest x / scale, halves to the even
-// code.  Both are decided exactly: a quotient by 6 never rounds onto a
-// midpoint of the e4m3 grid that it is not on, and x is compared with the
-// products midpoint * scale, which have at most 7 significant bits, instead of
-// a rounded quotient with the midpoints.  A NaN or infinity makes the scale
-// NaN: the whole group then reads back as NaN.
+// code.  Both come out exactly.  A quotient a / b of fp32 numbers is on a
+// midpoint m of either grid (at most 5 significant bits) or at least 0.53 of
+// fp32's steps away from it, as a and m * b are fp32 numbers too; so it is
+// enough to round the quotient correctly, and then to the grid.  For the
+// codes the reciprocal's product is corrected once by its exact remainder,
+// which leaves an error of 2^-47 before the rounding.  Comparing x with the
+// seven products midpoint * scale instead (exact as well) took 31 us where
+// this takes 14 (8 prompts, 8,300 tokens of 8 heads, d = 128): 21 integer
+// instructions an element at half rate.  A NaN or infinity makes the scale NaN:
+// the whole group then reads back as NaN.
 __device__ __forceinline__ void quantize16(float (&x)[16], int neg_log2, uint2& codes, uint32_t& scale) {
   float top = 0.f;
-  bool bad = false;
-  const float f = __int_as_float((127 + neg_log2) << 23);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-    x[i] *= f;   // a power of two; past the range it saturates below
-    top = fmaxf(top, fabsf(x[i]));
+  for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+  if (!(top <= 3.402823466e38f)) {
+    scale = 0x7Fu;
+    codes = make_uint2(0u, 0u);
+    return;
   }
-  const float want = __fdiv_rn(top, 6.f);
-  unsigned short two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(want));
-  scale = two & 0x7Fu;
-  uint32_t hs = e4m3x2(scale);
-  const float s = __half2float(__ushort_as_half((unsigned short)(hs & 0xFFFFu)));
-  const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s,
-              t5 = 3.5f * s, t6 = 5.f * s;
-  uint32_t w[2] = {0u, 0u};
+  if (neg_log2) {
+    const float f = __int_as_float((127 + neg_log2) << 23);
+    // far past saturation and far from overflow
+    const float most = 1.2e28f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float a = fabsf(x[i]);
-    uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
-    if (s == 0.f) c = 0;
-    c |= x[i] < 0.f ? 8u : 0u;
-    w[i >> 3] |= c << (4 * (i & 7));
+    for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -most), most) * f;
+    top = fminf(top, most) * f;
+  }
+  unsigned short two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(__fdiv_rn(top, 6.f)));
+  scale = two & 0x7Fu;
+  const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2(scale) & 0xFFFFu)));
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;   // a scale of 0 makes every code 0
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = x[8 * i + j], q = v * inv;
+      y[j] = fmaf(fmaf(-q, s, v), inv, q);
+    }
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w[i])
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   }
   codes = make_uint2(w[0], w[1]);
-  if (bad) { scale = 0x7Fu; codes = make_uint2(0u, 0u); }
 }
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendSmemSeq = 512;   // offsets kept in shared memory up to this many sequences
 
-// One thread per 16 dims of one token's key or value (one KV head).  The
+// One thread per 16 dims of one token's key and value (one KV head).  The
 // input is read once and 9 bytes written for its 32 or 64; threads of a warp
 // hold consecutive groups of the token, so reads are contiguous and a row's
 // codes are written as whole 32-byte sectors.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads)
-    kv4_append_kernel(Kv4 c, const uint8_t* k, const uint8_t* v, int dtype,
-                      size_t k_stride, size_t v_stride, const int32_t* offsets,
-                      int n_tokens, int k_neg, int v_neg) {
+    kv4_append_kernel(Kv4 c, const uint8_t* k, const uint8_t* v, int dtype, size_t k_stride, size_t v_stride,
+                      const int32_t* offsets, int n_tokens, int k_neg, int v_neg) {
   using S = Kv4Shape<D>;
   __shared__ int32_t offs[kAppendSmemSeq + 1];
   pdl_trigger();
@@ -143,19 +159,22 @@ __global__ void __launch_bounds__(kAppendThreads)
     __syncthreads();
   }
   constexpr int G = D / kKv4Group;
-  const int per = c.heads * 2 * G;   // threads of a token
-  const long long id = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-  const long long tok = id / per;
+  const uint32_t per = c.heads * G;   // threads of a token
+  const uint32_t id = blockIdx.x * kAppendThreads + threadIdx.x;
+  const int tok = (int)(id / per);
   if (tok >= n_tokens) return;
-  int r = (int)(id - tok * per);
-  const int g = r % G;
-  r /= G;
-  const int head = r % c.heads, which = r / c.heads;
+  const uint32_t part = id - tok * per;
+  const int head = part / G, g = part % G;
+  // the input does not depend on where it goes: in flight during the search
+  const size_t at_dim = (size_t)(head * D + g * kKv4Group) * (dtype == MK_DTYPE_F32 ? 4 : 2);
+  float x[2][16];
+  load16(k + (size_t)tok * k_stride + at_dim, dtype, x[0]);
+  load16(v + (size_t)tok * v_stride + at_dim, dtype, x[1]);
   auto at = [&](int i) { return near ? offs[i] : __ldcg(offsets + i); };
-  int lo = 0, hi = c.n_seq;   // the last sequence whose offset is <= tok
+  int lo = 0, hi = c.n_seq - 1;   // the last sequence whose offset is <= tok
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (mid < c.n_seq && at(mid) <= tok) lo = mid; else hi = mid - 1;
+    if (at(mid) <= tok) lo = mid; else hi = mid - 1;
   }
   const int first = at(lo), end = at(lo + 1);
   if (tok < first || tok >= end) return;   // before the first sequence or behind the last
@@ -164,20 +183,17 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int lp = (int)slot / c.page_tokens, in = (int)slot - lp * c.page_tokens;
   const int page = c.page(lo, lp);
   if (page < 0) return;
-  const int esz = dtype == MK_DTYPE_F32 ? 4 : 2;
-  float x[16];
-  load16((which ? v + (size_t)tok * v_stride : k + (size_t)tok * k_stride) +
-             (size_t)(head * D + g * kKv4Group) * esz,
-         dtype, x);
-  uint2 codes;
-  uint32_t scale;
-  quantize16(x, which ? v_neg : k_neg, codes, scale);
   uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
   const int row = in % kKv4Block;
-  *reinterpret_cast<uint2*>(b + (which ? S::kVc : 0) + row * S::kCodes + g * 8) = codes;
-  b[(which ? S::kVs : S::kKs) + row * S::kScales + g] = (uint8_t)scale;
-  if (c.scores && !which && g == 0)
-    c.scores[((size_t)lo * c.heads + head) * c.capacity() + slot] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint2 codes;
+    uint32_t scale;
+    quantize16(x[i], i ? v_neg : k_neg, codes, scale);
+    *reinterpret_cast<uint2*>(b + (i ? S::kVc : 0) + row * S::kCodes + g * 8) = codes;
+    b[(i ? S::kVs : S::kKs) + row * S::kScales + g] = (uint8_t)scale;
+  }
+  if (c.scores && g == 0) c.scores[((size_t)lo * c.heads + head) * c.capacity() + slot] = 0.f;
 }
 
 // -------------------------------------------------------------------- read
@@ -263,81 +279,156 @@ __device__ __forceinline__ uint32_t score_key(float f) {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelCtas = 8;   // most CTAs of a head: a portable cluster
 
-// Sum of one value per thread over the block, to every thread.  `buf` holds
-// two rows that calls alternate between, so one barrier a call is enough.
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*buf)[kSelWarps], int& flip) {
-  v = __reduce_add_sync(0xFFFFFFFFu, v);
-  if ((threadIdx.x & 31) == 0) buf[flip][threadIdx.x >> 5] = v;
-  __syncthreads();
-  const uint32_t t = __reduce_add_sync(0xFFFFFFFFu, buf[flip][threadIdx.x & 31]);
-  flip ^= 1;
-  return t;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store_peer(void* mine, int rank, unsigned long long v) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(b), "l"(v) : "memory");
 }
 
-// Which slots a head keeps.  One CTA per (sequence, KV head): the `take`
-// highest scores between the protected ends.  The threshold -- the highest T
-// with at least `take` keys >= T -- is found bit by bit from the top, each bit
-// one count over the keys, which stay in registers up to KPT * 1024 of them
-// (longer heads read theirs from L2 again for each bit).  A histogram per
-// digit would need fewer passes, but accumulated weights share their
-// exponents, so its shared-memory adds would run one after another on a few
-// bins.  The search stops at the first T with exactly `take` keys above.
-// Slots above T, and the lowest of those on it, are then written in slot
-// order by one prefix sum: position = (# above before) + min(# equal before,
-// equals wanted).
+// Sums over a head's CTAs of three counts below 2^21 each, in 21 bits of 64.
+// Rows that calls alternate between, so that a fast warp's or CTA's next
+// numbers do not meet a slow one's reading.
+struct SelShared {
+  unsigned long long warp[2][kSelWarps];
+  unsigned long long cta[2][kSelCtas];
+};
+__device__ __forceinline__ unsigned long long three(uint32_t a, uint32_t b, uint32_t c) {
+  return (unsigned long long)a | (unsigned long long)b << 21 | (unsigned long long)c << 42;
+}
+__device__ __forceinline__ uint32_t one_of(unsigned long long v, int i) { return (uint32_t)(v >> (21 * i)) & 0x1FFFFFu; }
+__device__ __forceinline__ unsigned long long warp_three(unsigned long long v) {
+  return three(__reduce_add_sync(0xFFFFFFFFu, one_of(v, 0)), __reduce_add_sync(0xFFFFFFFFu, one_of(v, 1)),
+               __reduce_add_sync(0xFFFFFFFFu, one_of(v, 2)));
+}
+
+// `v`: this warp's counts.  Every thread of the cluster gets the sum of all,
+// and that of the CTAs before its own.
+__device__ __forceinline__ unsigned long long sum_all(unsigned long long v, SelShared& s, int& flip, int rank,
+                                                      int ctas, unsigned long long* before = nullptr) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) s.warp[flip][warp] = v;
+  __syncthreads();
+  unsigned long long all = 0ull, low = 0ull;
+  if (ctas == 1) {
+    all = warp_three(s.warp[flip][lane]);
+  } else {
+    if (warp == 0) {
+      const unsigned long long t = warp_three(s.warp[flip][lane]);
+      if (lane < ctas) store_peer(&s.cta[flip][rank], lane, t);
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int i = 0; i < ctas; ++i) {
+      const unsigned long long t = s.cta[flip][i];
+      all += t;
+      if (i < rank) low += t;
+    }
+  }
+  if (before) *before = low;
+  flip ^= 1;
+  return all;
+}
+
+// Which slots a head keeps: the `take` highest scores between the protected
+// ends.  A head's keys are cut into contiguous parts, one for each CTA of a
+// cluster, and stay in registers (KPT a thread; longer parts are read from L2
+// again for each step).  The threshold -- the highest T with at least `take` keys
+// >= T -- is found two bits at a time from the top: one pass counts the keys
+// above three candidates, three 21-bit counters in a 64-bit sum, over the
+// cluster's shared memory.  A count is bound by the integer pipe (3
+// instructions a key and candidate, 64 lanes a clock and SM: 32,768 keys on
+// one SM took 47 us), so it pays to spread a head; each step costs ~600 clocks
+// of barriers, so two bits a step beat one (half the steps) and three (seven
+// candidates for three bits).  A histogram per digit would need fewer passes,
+// but accumulated weights share their exponents, so its shared-memory adds run
+// one after another on a few bins.  The search stops at the first T with
+// exactly `take` keys above.  Slots above T, and the lowest of those on it, are
+// then written in slot order by prefix sums:
+// position = (# above before) + min(# equal before, equals wanted).
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads, 1)
-    kv4_select_kernel(Kv4 c, int budget, int first, int last, int32_t* kept) {
-  __shared__ uint32_t sums[2][kSelWarps];
-  __shared__ uint32_t cnt[KPT][kSelWarps];
-  __shared__ uint32_t carry[2];
+    kv4_select_kernel(Kv4 c, int budget, int first, int last, int ctas, int32_t* kept) {
+  __shared__ SelShared sh;
+  __shared__ uint32_t cnt[KPT][kSelWarps], sums[kSelWarps];
   pdl_trigger();
   pdl_wait();
-  const int head = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+  const int rank = ctas > 1 ? blockIdx.x % ctas : 0, head = blockIdx.x / ctas, s = blockIdx.y, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   const int n = c.len(s);
   int32_t* out = kept + ((size_t)s * c.heads + head) * budget;
+  const int step = ctas * kSelThreads, from = rank * kSelThreads + tid;
   if (n <= budget) {
-    for (int i = tid; i < budget; i += kSelThreads) out[i] = i < n ? i : -1;
+    for (int i = from; i < budget; i += step) out[i] = i < n ? i : -1;
     return;
   }
-  const float* sc = c.scores + ((size_t)s * c.heads + head) * c.capacity() + first;
-  const int m = n - first - last, take = budget - first - last;   // take < m
-  for (int i = tid; i < first; i += kSelThreads) out[i] = i;
-  for (int i = tid; i < last; i += kSelThreads) out[budget - last + i] = n - last + i;
+  const int m_all = n - first - last, take = budget - first - last;   // take < m_all
+  for (int i = from; i < first; i += step) out[i] = i;
+  for (int i = from; i < last; i += step) out[budget - last + i] = n - last + i;
   if (take == 0) return;
-  const bool whole = m <= KPT * kSelThreads;
+  if (ctas > 1) cluster_arrive();   // every CTA has begun before another writes its shared memory
+  // this CTA's part
+  const int part = (m_all + ctas - 1) / ctas, p0 = min(m_all, rank * part), m = min(m_all, p0 + part) - p0;
+  const float* sc = c.scores + ((size_t)s * c.heads + head) * c.capacity() + first + p0;
+  const bool whole = part <= KPT * kSelThreads;
   uint32_t key[KPT];
 #pragma unroll
   for (int j = 0; j < KPT; ++j) {
     const int i = j * kSelThreads + tid;
     key[j] = whole && i < m ? score_key(__ldcg(sc + i)) : 0u;
   }
+  if (ctas > 1) cluster_wait();
   int flip = 0;
-  // keys >= t (t > 0, so the padding zeros never count)
-  auto at_least = [&](uint32_t t) {
-    uint32_t v = 0;
-    if (whole) {
+  // keys >= a, b, c in 21 bits each, a <= b <= c; a > 0, so the padding zeros never count
+  auto at_least = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
+    if (whole) {   // three counts of at most 512 a warp in one word
+      uint32_t v = 0;
 #pragma unroll
-      for (int j = 0; j < KPT; ++j) v += key[j] >= t;
-    } else {
-      for (int i = tid; i < m; i += kSelThreads) v += score_key(__ldcg(sc + i)) >= t;
+      for (int j = 0; j < KPT; ++j)
+        v += (key[j] >= t1 ? 1u : 0u) + (key[j] >= t2 ? 1u << 10 : 0u) + (key[j] >= t3 ? 1u << 20 : 0u);
+      v = __reduce_add_sync(0xFFFFFFFFu, v);
+      return sum_all(three(v & 1023u, v >> 10 & 1023u, v >> 20), sh, flip, rank, ctas);
     }
-    return block_sum(v, sums, flip);
+    uint32_t v1 = 0, v2 = 0, v3 = 0;
+    for (int i = tid; i < m; i += kSelThreads) {
+      const uint32_t k = score_key(__ldcg(sc + i));
+      v1 += k >= t1; v2 += k >= t2; v3 += k >= t3;
+    }
+    return sum_all(warp_three(three(v1, v2, v3)), sh, flip, rank, ctas);
   };
-  uint32_t T = 0, have = (uint32_t)m;
-  for (int bit = 31; bit >= 0 && have != (uint32_t)take; --bit) {
-    const uint32_t t = T | (1u << bit), a = at_least(t);
-    if (a >= (uint32_t)take) { T = t; have = a; }
+  uint32_t T = 0, have = (uint32_t)m_all;
+  for (int bit = 30; bit >= 0 && have != (uint32_t)take; bit -= 2) {
+    const unsigned long long a = at_least(T | 1u << bit, T | 2u << bit, T | 3u << bit);
+#pragma unroll
+    for (int k = 2; k >= 0; --k)
+      if (one_of(a, k) >= (uint32_t)take) { T |= (uint32_t)(k + 1) << bit; have = one_of(a, k); break; }
   }
   // `have` keys are >= T.  Exactly `take`: all of them are kept and none is on
   // the border; otherwise T is a key's value and the lowest slots on it fill up.
-  uint32_t above = have;
   const bool exact = have == (uint32_t)take;
-  if (!exact) above = T == 0xFFFFFFFFu ? 0u : at_least(T + 1u);
-  const uint32_t equals = exact ? 0u : (uint32_t)take - above;
-  if (tid == 0) carry[0] = carry[1] = 0u;
+  auto above = [&](uint32_t k) { return exact ? k >= T : k > T; };
+  uint32_t gt = 0, eq = 0;
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const bool in = j * kSelThreads + tid < m;
+      gt += in && above(key[j]);
+      eq += in && !exact && key[j] == T;
+    }
+  } else {
+    for (int i = tid; i < m; i += kSelThreads) {
+      const uint32_t k = score_key(__ldcg(sc + i));
+      gt += above(k);
+      eq += !exact && k == T;
+    }
+  }
+  unsigned long long low;
+  const unsigned long long sum = sum_all(warp_three(three(gt, eq, 0u)), sh, flip, rank, ctas, &low);
+  uint32_t base_gt = one_of(low, 0), base_eq = one_of(low, 1);   // in the CTAs before
+  const uint32_t equals = (uint32_t)take - one_of(sum, 0);
   for (int base = 0; base < m; base += KPT * kSelThreads) {
     if (!whole) {
 #pragma unroll
@@ -346,18 +437,18 @@ __global__ void __launch_bounds__(kSelThreads, 1)
         key[j] = i < m ? score_key(__ldcg(sc + i)) : 0u;
       }
     }
-    uint32_t gt = 0, eq = 0;   // a bit per j
+    uint32_t g_bits = 0, e_bits = 0;   // a bit per j
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
       const bool in = base + j * kSelThreads + tid < m;
-      const bool g = in && (exact ? key[j] >= T : key[j] > T), e = in && !exact && key[j] == T;
-      gt |= (uint32_t)g << j;
-      eq |= (uint32_t)e << j;
+      const bool g = in && above(key[j]), e = in && !exact && key[j] == T;
+      g_bits |= (uint32_t)g << j;
+      e_bits |= (uint32_t)e << j;
       const uint32_t bg = __ballot_sync(0xFFFFFFFFu, g), be = __ballot_sync(0xFFFFFFFFu, e);
       if (lane == 0) cnt[j][warp] = (uint32_t)__popc(bg) << 16 | (uint32_t)__popc(be);
     }
     __syncthreads();
-    // exclusive prefix over (j, warp), counts above in the high half (at most 32,768 of each)
+    // exclusive prefix over (j, warp), counts above in the high half (at most 16,384 of each)
     const bool mine = tid < KPT * kSelWarps;
     const uint32_t own = mine ? cnt[tid >> 5][lane] : 0u;
     uint32_t inc = own;
@@ -366,25 +457,23 @@ __global__ void __launch_bounds__(kSelThreads, 1)
       const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += up;
     }
-    if (lane == 31) sums[flip][warp] = inc;
+    if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    uint32_t before = lane < warp ? sums[flip][lane] : 0u;
-    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0u);
     if (mine) cnt[tid >> 5][lane] = before + inc - own;
-    const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, sums[flip][lane]);
-    flip ^= 1;
-    const uint32_t cg = carry[0], ce = carry[1];
+    const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, sums[lane]);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
-      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt >> j & 1u),
-                     be = __ballot_sync(0xFFFFFFFFu, eq >> j & 1u);
+      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, g_bits >> j & 1u),
+                     be = __ballot_sync(0xFFFFFFFFu, e_bits >> j & 1u);
       const uint32_t lt = (1u << lane) - 1u, p = cnt[j][warp];
-      const uint32_t ng = cg + (p >> 16) + __popc(bg & lt), ne = ce + (p & 0xFFFFu) + __popc(be & lt);
-      if ((gt >> j & 1u) || ((eq >> j & 1u) && ne < equals))
-        out[first + ng + min(ne, equals)] = first + base + j * kSelThreads + tid;
+      const uint32_t ng = base_gt + (p >> 16) + __popc(bg & lt), ne = base_eq + (p & 0xFFFFu) + __popc(be & lt);
+      if ((g_bits >> j & 1u) || ((e_bits >> j & 1u) && ne < equals))
+        out[first + ng + min(ne, equals)] = first + p0 + base + j * kSelThreads + tid;
     }
-    if (tid == 0) { carry[0] = cg + (all >> 16); carry[1] = ce + (all & 0xFFFFu); }
+    base_gt += all >> 16;
+    base_eq += all & 0xFFFFu;
     __syncthreads();
   }
 }
@@ -476,9 +565,9 @@ extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const
       (k_stride * esz) % 16 || (v_stride * esz) % 16)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "keys and values of a token are 16-byte aligned");
   const Kv4 c = kv4_of(cache);
-  const long long threads = (long long)n_tokens * c.heads * 2 * (cache->head_dim / kKv4Group);
+  const long long threads = (long long)n_tokens * c.heads * (cache->head_dim / kKv4Group);
   const long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
-  if (blocks > 0x7FFFFFFFll) return kv4_fail(MK_ERR_INVALID_ARG, who, "too many tokens in one call");
+  if (threads > 0x7FFFFFFFll) return kv4_fail(MK_ERR_INVALID_ARG, who, "too many tokens in one call");
   const uint8_t* k = static_cast<const uint8_t*>(k_dev);
   const uint8_t* v = static_cast<const uint8_t*>(v_dev);
   const size_t ks = (size_t)k_stride * esz, vs = (size_t)v_stride * esz;
@@ -521,6 +610,8 @@ extern "C" int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, in
   if (!src->scores_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "the source has scores");
   if (budget < 1 || budget > (long long)dst->pages_per_seq * dst->page_tokens)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "budget is 1 to the destination's capacity");
+  if ((long long)src->pages_per_seq * src->page_tokens > (1 << 21) - 1)
+    return kv4_fail(MK_ERR_UNSUPPORTED, who, "a sequence of the source holds fewer than 2^21 keys");
   if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > budget)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "keep_first + keep_last is 0 to budget");
   if (!kept_dev || (reinterpret_cast<uintptr_t>(kept_dev) & 3u))
@@ -530,11 +621,15 @@ extern "C" int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, in
     return kv4_fail(MK_ERR_INVALID_ARG, who, "the destination has pages and scores of its own");
   const Kv4 a = kv4_of(src), b = kv4_of(dst);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // as many registers of keys as the longest head can need
+  // 2 or 4 keys a thread in as many CTAs as the longest head can need (the fewer keys
+  // an SM counts, the faster); past 8 CTAs of them 16 keys a thread
+  const int per_cta = 4 * kSelThreads;
+  int ctas = 1;
+  while (ctas < kSelCtas && (long long)ctas * per_cta < a.capacity()) ctas <<= 1;
   auto select = a.capacity() <= 2 * kSelThreads ? kv4_select_kernel<2>
-                : a.capacity() <= 8 * kSelThreads ? kv4_select_kernel<8> : kv4_select_kernel<32>;
-  cudaError_t e = pdl_launch(select, dim3(a.heads, a.n_seq), dim3(kSelThreads), 0, st, a, budget, keep_first,
-                             keep_last, kept_dev);
+                : (long long)ctas * per_cta < a.capacity() ? kv4_select_kernel<16> : kv4_select_kernel<4>;
+  cudaError_t e = pdl_launch_cluster(select, dim3(a.heads * ctas, a.n_seq), dim3(kSelThreads), ctas, st, a, budget,
+                                     keep_first, keep_last, ctas, kept_dev);
   if (e != cudaSuccess) return kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
   const int rows = kMoveThreads / kMoveLanes * kMoveRows;
   auto move = src->head_dim == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>;
