@@ -111,9 +111,14 @@ struct AttnArgs {
   // workspace
   float* warp_part;      // [max_ctas * kWarps][R][d + 2]: a warp's first, unfinished piece
   float* cta_part;       // [max_ctas][2][R][d + 2]: a CTA's first and last, unfinished
-  float* stats;          // [n_seq * tiles * heads][R][2]: max and sum of rows that one CTA finished
+  float2* stats;         // [n_seq * tiles * heads][R]: max and sum of rows that one CTA finished
   float* s_all;          // [units][32][stored rows]: scores in log2 units
   int32_t s_rows;
+  // what the first kernel found out, for the second
+  int4* line;            // total, each, rest, ctas (Line)
+  int4* edges;           // [max_ctas]: the item that a CTA leaves unfinished: sequence, item, first block's
+                         // unit, blocks; item -1: none
+  int4* begins;          // [max_ctas]: where a CTA's share of the scores begins: sequence, its first unit, keys
 };
 
 // Starting an item (its pages, its queries, its result) takes about as long as
@@ -135,13 +140,16 @@ struct Line {
   __device__ __forceinline__ int cta_of(int u) const { return range_of(u) / kWarps; }
 };
 
+// First unit of a CTA's share of the scores.
+__device__ __forceinline__ int scores_cut(int total, int i, int ctas) { return (int)((long long)total * i / ctas); }
+
 __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / kKv4Block; }
 __device__ __forceinline__ int units_of(int n) { return n ? blocks_of(n) + kStart : 0; }
 
 // One warp's view of the line: lane i holds a run of consecutive sequences, `base`
-// the units before them.
+// the units before them, n the keys of the first.
 struct Scan {
-  int32_t s0, s1, base, mine;
+  int32_t s0, s1, base, mine, n;
 };
 
 __device__ __forceinline__ Scan line_scan(const AttnArgs& a, Line& l) {
@@ -150,9 +158,10 @@ __device__ __forceinline__ Scan line_scan(const AttnArgs& a, Line& l) {
   Scan z;
   z.s0 = min(a.c.n_seq, lane * run);
   z.s1 = min(a.c.n_seq, z.s0 + run);
-  z.mine = 0;
+  z.n = z.s0 < z.s1 ? a.c.len(z.s0) : 0;
+  z.mine = units_of(z.n);
 #pragma unroll 4
-  for (int s = z.s0; s < z.s1; ++s) z.mine += units_of(a.c.len(s));
+  for (int s = z.s0 + 1; s < z.s1; ++s) z.mine += units_of(a.c.len(s));
   z.mine *= items;
   int inc = z.mine;
 #pragma unroll
@@ -170,21 +179,23 @@ __device__ __forceinline__ Scan line_scan(const AttnArgs& a, Line& l) {
   return z;
 }
 
-// The sequence that unit u lies in, and the units before it.
-__device__ __forceinline__ void line_find(const AttnArgs& a, const Scan& z, int u, int& seq, int& start) {
+// The sequence that unit u lies in, the units before it and its keys.
+__device__ __forceinline__ void line_find(const AttnArgs& a, const Scan& z, int u, int& seq, int& start, int& n) {
   const bool here = u >= z.base && u < z.base + z.mine;
-  int s = z.s0, b = z.base;
-  if (here) {
+  int s = z.s0, b = z.base, m = z.n;
+  if (here && z.s0 + 1 < z.s1) {
     const int items = a.tiles * a.c.heads;
-    for (; s + 1 < z.s1; ++s) {
-      const int n = units_of(a.c.len(s)) * items;
-      if (u < b + n) break;
-      b += n;
+    for (;;) {
+      const int len = units_of(m) * items;
+      if (u < b + len) break;
+      b += len;
+      m = a.c.len(++s);
     }
   }
-  const int who = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
-  seq = __shfl_sync(0xFFFFFFFFu, s, max(who, 0));
-  start = __shfl_sync(0xFFFFFFFFu, b, max(who, 0));
+  const int who = max(__ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1, 0);
+  seq = __shfl_sync(0xFFFFFFFFu, s, who);
+  start = __shfl_sync(0xFFFFFFFFu, b, who);
+  n = __shfl_sync(0xFFFFFFFFu, m, who);
 }
 
 // Four (or N) consecutive output elements, rounded once.
@@ -251,10 +262,10 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   constexpr int kPart = R * (D + 2);
   static_assert(kPart * 4 <= kStages * S::kBytes, "a warp's last piece takes the place of its ring");
   extern __shared__ __align__(16) uint8_t ring_all[];
-  // pieces that a warp leaves: [0] its first, in global memory, [1] its last, in its ring's place
-  __shared__ int piece_item[2][kWarps];    // -1: none
-  __shared__ int piece_seq[2][kWarps], piece_begins[2][kWarps];
-  __shared__ float weight[kWarps + 1][R], total[R];
+  // pieces that a warp leaves: even its first, in global memory, odd its last, in its ring's place
+  __shared__ int4 piece_of[2 * kWarps];    // sequence, item (-1: none), first block's unit, blocks
+  __shared__ float piece_max[2 * kWarps][R], piece_sum[2 * kWarps][R];
+  __shared__ float weight[kWarps][R], total[R];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
@@ -262,27 +273,30 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   const Scan scan = line_scan(a, line);
   const int items = a.tiles * a.c.heads;
 
-  // sequences without a key: their outputs are zero and no unit covers them
-  for (int s = blockIdx.x; s < a.c.n_seq; s += gridDim.x) {
-    if (a.c.len(s) > 0) continue;
-    const size_t n = (size_t)a.rows * a.c.heads * D;
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    for (size_t i = threadIdx.x * 4; i < n; i += kThreadsA * 4) store_out<DT, 4>(a.out, s * n + i, zero);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.line = make_int4(line.total, line.each, line.rest, line.ctas);
+  if (a.accumulate && warp == kWarps - 1) {
+    // units of all row tiles share their keys: the line without row tiles
+    const int v = scores_cut(line.total / a.tiles, blockIdx.x, gridDim.x);
+    int4 z;
+    line_find(a, scan, v * a.tiles, z.x, z.y, z.z);
+    if (lane == 0) a.begins[blockIdx.x] = z;
   }
-  if ((int)blockIdx.x >= line.ctas) return;
+  if ((int)blockIdx.x >= line.ctas) {
+    if (threadIdx.x == 0) a.edges[blockIdx.x] = make_int4(0, -1, 0, 0);
+    return;
+  }
 
   // this warp's range
   int u = line.cut(blockIdx.x * kWarps + warp);
   const int u_end = line.cut(blockIdx.x * kWarps + warp + 1);
-  int seq = 0, start = 0;
-  if (u < u_end) line_find(a, scan, u, seq, start);
-  if (lane < 2) piece_item[lane][warp] = -1;
+  int seq = 0, start = 0, n = 0;
+  if (u < u_end) line_find(a, scan, u, seq, start, n);
+  if (lane < 2) piece_of[2 * warp + lane] = make_int4(0, -1, 0, 0);
 
   uint8_t* ring = ring_all + (size_t)warp * kStages * S::kBytes;
   const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const int per = a.c.page_tokens / kKv4Block;
 
-  int n = u < u_end ? a.c.len(seq) : 0;
   while (u < u_end) {
     // ---- the piece of one item that this range covers
     while (n == 0) n = a.c.len(++seq);   // u < total: a sequence with keys follows
@@ -654,76 +668,84 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
             store_out<DT, D / 8>(a.out, at + r * (D / 8), y);
           }
           if (a.accumulate && r == 0) {
-            float2* st = reinterpret_cast<float2*>(a.stats) + ((size_t)this_seq * items + item) * R + col;
-            *st = make_float2(ref[nt][c], x);
+            a.stats[((size_t)this_seq * items + item) * R + col] = make_float2(ref[nt][c], x);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
             *reinterpret_cast<float4*>(to + col * D + r * (D / 8) + 4 * i) =
                 make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          if (r == 0) { to[R * D + col] = ref[nt][c]; to[R * D + R + col] = x; }
+          if (r == 0) {
+            piece_max[2 * warp + !ends][col] = ref[nt][c];
+            piece_sum[2 * warp + !ends][col] = x;
+          }
         }
       }
-    if (lane == 0 && !(begins && ends)) {
-      const int last = !ends;
-      piece_item[last][warp] = item;
-      piece_seq[last][warp] = this_seq;
-      piece_begins[last][warp] = begins;
-    }
+    if (lane == 0 && !(begins && ends))
+      piece_of[2 * warp + !ends] = make_int4(this_seq, item, item_at + kStart, begins ? -nb : nb);   // < 0: begins here
   }
   __syncthreads();
 
   // ---- pieces of the CTA's warps that belong together, in order: the last of
   // a warp, those of warps that lie whole in the item, the first of the one
   // where it ends
-  auto piece = [&](int code) -> const float* {   // code: 2 * warp + last
-    const int w = code >> 1;
-    return code & 1 ? reinterpret_cast<const float*>(ring_all + (size_t)w * kStages * S::kBytes)
-                    : part_at<D, R>(a.warp_part, blockIdx.x * kWarps + w);
-  };
-  // pieces `first`, then the last ones of the warps after it, `count` in all, the
-  // final one the first piece of its warp if the item ends here
-  auto merge = [&](int first, int count, bool ends) {
-    const int w0 = first >> 1, fin = ends ? 2 * (w0 + count - 1) : 2 * (w0 + count - 1) + 1;
-    const int seq = piece_seq[first & 1][w0], item = piece_item[first & 1][w0];
-    const bool begins = piece_begins[first & 1][w0];
-    const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
+  // pieces [first, first + count) of those in `mask`; the final one ends the item, or not
+  auto merge = [&](uint32_t mask, int count, bool ends) {
+    int code[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      code[i] = i < count ? __ffs(mask) - 1 : 0;
+      mask &= mask - 1u;
+    }
+    const int4 who = piece_of[code[0]];
+    const bool done = who.w < 0 && ends;   // begins and ends in this CTA
+    const int tile = who.y / a.c.heads, kvh = who.y - tile * a.c.heads;
     const int rows = min(R, a.rows - tile * R);
-    auto nth = [&](int i) { return piece(i == count - 1 && count > 1 ? fin : i == 0 ? first : 2 * (w0 + i) + 1); };
     float* slot = part_at<D, R>(a.cta_part, blockIdx.x * 2 + (ends ? 0 : 1));
-    __syncthreads();   // the last merge is done with the weights
     if ((int)threadIdx.x < R) {
       const int row = threadIdx.x;
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < count; ++i) m = fmaxf(m, nth(i)[R * D + row]);
-      for (int i = 0; i < count; ++i) {
-        const float f = rescale(nth(i)[R * D + row], m);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i)
+        if (i < count) m = fmaxf(m, piece_max[code[i]][row]);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float f = i < count ? rescale(piece_max[code[i]][row], m) : 0.f;
         weight[i][row] = f;
-        l = fmaf(f, nth(i)[R * D + R + row], l);
+        if (i < count) l = fmaf(f, piece_sum[code[i]][row], l);
       }
       total[row] = l;
-      if (begins && ends) {
-        if (a.accumulate)
-          reinterpret_cast<float2*>(a.stats)[((size_t)seq * items + item) * R + row] = make_float2(m, l);
-      } else {
+      if (!done) {
         slot[R * D + row] = m;
         slot[R * D + R + row] = l;
+      } else if (a.accumulate) {
+        a.stats[((size_t)who.x * items + who.y) * R + row] = make_float2(m, l);
       }
     }
+    if (!ends && threadIdx.x == 0) a.edges[blockIdx.x] = make_int4(who.x, who.y, who.z, abs(who.w));
     __syncthreads();
     for (int e = threadIdx.x * 4; e < rows * D; e += kThreadsA * 4) {
       const int row = e / D;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < count; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(nth(i) + e);
-        const float f = weight[i][row];
-        x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]);
-        x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+      float4 v[kWarps];
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < count) {
+          const float* p = code[i] & 1 ? reinterpret_cast<const float*>(ring_all + (size_t)(code[i] >> 1) * kStages * S::kBytes)
+                                       : part_at<D, R>(a.warp_part, blockIdx.x * kWarps + (code[i] >> 1));
+          v[i] = *reinterpret_cast<const float4*>(p + e);
+        }
       }
-      if (begins && ends) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float f = weight[i][row];   // 0 behind the last
+        x[0] = fmaf(f, v[i].x, x[0]); x[1] = fmaf(f, v[i].y, x[1]);
+        x[2] = fmaf(f, v[i].z, x[2]); x[3] = fmaf(f, v[i].w, x[3]);
+      }
+      if (done) {
         size_t at;
-        out_row<D, R>(a, seq, tile, kvh, row, at);
+        out_row<D, R>(a, who.x, tile, kvh, row, at);
         const float f = inverse(a, total[row]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] *= f;
@@ -732,95 +754,109 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
         *reinterpret_cast<float4*>(slot + e) = make_float4(x[0], x[1], x[2], x[3]);
       }
     }
+    __syncthreads();   // the weights are free
   };
-  int open = -1, count = 0;
-#pragma unroll 1
-  for (int code = 0; code < 2 * kWarps; ++code) {
-    const int last = code & 1;
-    if (piece_item[last][code >> 1] < 0) continue;
-    if (count == 0) open = code;
-    ++count;
-    if (!last) { merge(open, count, true); count = 0; }
+  uint32_t pieces = __ballot_sync(0xFFFFFFFFu, lane < 2 * kWarps && piece_of[lane & (2 * kWarps - 1)].y >= 0);
+  bool open = false;
+  while (pieces) {   // up to the next first piece (an even one), which ends its item
+    const uint32_t even = pieces & 0x55555555u;
+    const uint32_t now = even ? pieces & (even ^ (even - 1u)) : pieces;
+    merge(now, __popc(now), even != 0u);
+    pieces &= ~now;
+    open = even == 0u;
   }
-  if (count) merge(open, count, false);
+  if (!open && threadIdx.x == 0) a.edges[blockIdx.x] = make_int4(0, -1, 0, 0);
 }
 
-// ---- what CTAs share.  The CTAs whose ranges begin strictly inside an item
-// split its merge among them; then, if asked, every key's weights go to its
-// score.
+// ---- what CTAs share.  Blocks [0, max_ctas): the CTAs that leave an item
+// unfinished split its merge among them (and zero what no unit covers).
+// Blocks behind them, if asked: every key's weights go to its score.  All they
+// read of the first kernel's is found by one load, so that the rest is in
+// flight at once.
 constexpr int kThreadsM = 256;
 constexpr int kWarpsM = kThreadsM / 32;
+
+// Running (maximum, sum) pairs of two partials.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2);
+  l = l * rescale(m, top) + l2 * rescale(m2, top);
+  m = top;
+}
 
 template <int D, int DT, int R>
 __global__ void __launch_bounds__(kThreadsM) kv4_attn_merge_kernel(const AttnArgs a) {
   __shared__ float2 stat[kMaxRows];
   pdl_trigger();
   pdl_wait();
-  Line line;
-  const Scan scan = line_scan(a, line);
-  if (line.total == 0) return;
+  const bool merges = (int)blockIdx.x < a.max_ctas;
+  const int me = merges ? blockIdx.x : blockIdx.x - a.max_ctas;
+  const int4 head = __ldcg(a.line), rec = __ldcg((merges ? a.edges : a.begins) + me);
+  const Line line = {head.x, head.y, head.z, head.w};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = a.tiles * a.c.heads;
   // a CTA's piece of an item that goes on behind it is its last, else its first
   auto slot_of = [&](int cta, int c1) { return part_at<D, R>(a.cta_part, cta * 2 + (cta < c1 ? 1 : 0)); };
 
-  if ((int)blockIdx.x + 1 < line.ctas) {
-    const int edge = line.cut((blockIdx.x + 1) * kWarps);   // where the next CTA begins
-    int seq, start;
-    line_find(a, scan, edge, seq, start);
-    const int nb = blocks_of(a.c.len(seq));
-    const int item = (edge - start) / (nb + kStart), i0 = start + item * (nb + kStart) + kStart;
-    if (edge > i0) {
-      const int c0 = line.cta_of(i0), c1 = line.cta_of(i0 + nb - 1);   // c0 <= blockIdx.x < c1
-      const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
-      const int fours = min(R, a.rows - tile * R) * D / 4, share = c1 - c0, me = blockIdx.x - c0;
-      const int e0 = fours * me / share, e1 = fours * (me + 1) / share;
-      // `wide` lanes to four elements, a partial each
-      int wide = 1;
-      while (wide < 32 && wide < c1 - c0 + 1) wide <<= 1;
-      const int sub = lane & (wide - 1), at_once = kWarpsM * (32 / wide);
-      for (int base = e0; base < e1; base += at_once) {   // the same number of rounds for every lane
-        const int e = base + warp * (32 / wide) + lane / wide;
-        const bool ok = e < e1;
-        const int row = ok ? e * 4 / D : 0;
-        float m = -INFINITY;
-        for (int i = c0 + sub; i <= c1; i += wide) m = fmaxf(m, __ldcg(slot_of(i, c1) + R * D + row));
-        for (int s = wide >> 1; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-        float x[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
-        if (ok) {
-          for (int i = c0 + sub; i <= c1; i += wide) {
-            const float* p = slot_of(i, c1);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
-            const float f = rescale(__ldcg(p + R * D + row), m);
-            x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]);
-            x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
-            x[4] = fmaf(f, __ldcg(p + R * D + R + row), x[4]);
-          }
-        }
-        for (int s = wide >> 1; s; s >>= 1)
-#pragma unroll
-          for (int k = 0; k < 5; ++k) x[k] += __shfl_xor_sync(0xFFFFFFFFu, x[k], s);
-        if (ok && sub == 0) {
-          size_t at;
-          out_row<D, R>(a, seq, tile, kvh, row, at);
-          const float f = inverse(a, x[4]);
-          const float y[4] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f};
-          store_out<DT, 4>(a.out, at + e * 4 - row * D, y);
+  if (merges) {
+    // sequences without a key: their outputs are zero and no unit covers them
+    for (int s = blockIdx.x; s < a.c.n_seq; s += a.max_ctas) {
+      if (a.c.len(s) > 0) continue;
+      const size_t n = (size_t)a.rows * a.c.heads * D;
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      for (size_t i = tid * 4; i < n; i += kThreadsM * 4) store_out<DT, 4>(a.out, s * n + i, zero);
+    }
+    if (rec.y < 0) return;
+    const int seq = rec.x, item = rec.y, i0 = rec.z, nb = rec.w;
+    const int c0 = line.cta_of(i0), c1 = line.cta_of(i0 + nb - 1);   // c0 <= me < c1
+    const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
+    const int fours = min(R, a.rows - tile * R) * D / 4, share = c1 - c0;
+    const int e0 = fours * (me - c0) / share, e1 = fours * (me - c0 + 1) / share;
+    // `wide` lanes to four elements, a partial each
+    int wide = 1;
+    while (wide < 32 && wide < c1 - c0 + 1) wide <<= 1;
+    const int sub = lane & (wide - 1), at_once = kWarpsM * (32 / wide);
+    for (int base = e0; base < e1; base += at_once) {   // the same number of rounds for every lane
+      const int e = base + warp * (32 / wide) + lane / wide;
+      const bool ok = e < e1;
+      const int row = ok ? e * 4 / D : 0;
+      float m = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (ok) {
+#pragma unroll 4
+        for (int i = c0 + sub; i <= c1; i += wide) {
+          const float* p = slot_of(i, c1);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + e);
+          const float m2 = __ldcg(p + R * D + row), l2 = __ldcg(p + R * D + R + row);
+          const float top = fmaxf(m, m2), f = rescale(m, top), g = rescale(m2, top);
+          m = top;
+          l = fmaf(g, l2, l * f);
+          x[0] = fmaf(g, v.x, x[0] * f); x[1] = fmaf(g, v.y, x[1] * f);
+          x[2] = fmaf(g, v.z, x[2] * f); x[3] = fmaf(g, v.w, x[3] * f);
         }
       }
+      for (int s = wide >> 1; s; s >>= 1) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, s), l2 = __shfl_xor_sync(0xFFFFFFFFu, l, s);
+        const float top = fmaxf(m, m2), f = rescale(m, top), g = rescale(m2, top);
+        m = top;
+        l = f * l + g * l2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = f * x[k] + g * __shfl_xor_sync(0xFFFFFFFFu, x[k], s);
+      }
+      if (ok && sub == 0) {
+        size_t at;
+        out_row<D, R>(a, seq, tile, kvh, row, at);
+        const float f = inverse(a, l);
+        const float y[4] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f};
+        store_out<DT, 4>(a.out, at + e * 4 - row * D, y);
+      }
     }
+    return;
   }
-  if (!a.accumulate) return;
 
-  // Units of all row tiles share their keys: the line without row tiles, in
-  // equal ranges of one CTA each.
   const int keys_total = line.total / a.tiles;
-  int v = (int)((long long)keys_total * blockIdx.x / gridDim.x);
-  const int v_end = (int)((long long)keys_total * (blockIdx.x + 1) / gridDim.x);
+  int v = scores_cut(keys_total, me, a.max_ctas);
+  const int v_end = scores_cut(keys_total, me + 1, a.max_ctas);
   if (v >= v_end) return;
-  int seq, start;   // start: in units of all row tiles
-  line_find(a, scan, v * a.tiles, seq, start);
-  int n = a.c.len(seq);
+  int seq = rec.x, start = rec.y, n = rec.z;   // start: in units of all row tiles
   while (v < v_end) {
     while (n == 0) n = a.c.len(++seq);
     const int nb = blocks_of(n), in_seq = v - start / a.tiles;
@@ -828,6 +864,23 @@ __global__ void __launch_bounds__(kThreadsM) kv4_attn_merge_kernel(const AttnArg
     const int stop = min(v_end, head_at + nb + kStart);
     const int b0 = max(v - head_at - kStart, 0), b1 = stop - head_at - kStart;
     if (b1 > b0) {
+      const int k0 = b0 * kKv4Block + tid, k_end = min(n, b1 * kKv4Block);
+      float* score = a.c.scores + ((size_t)seq * a.c.heads + kvh) * a.c.capacity();
+      // up to 8 rows: the scores of this thread's first keys load beside the statistics
+      constexpr int kAhead = R == 8 ? 4 : 0;
+      float2 s[kAhead + 1][4];
+      float old[kAhead + 1];
+      const float* s_at = a.s_all + (size_t)(start + kvh * (nb + kStart) + kStart) * kKv4Block * a.s_rows;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int key = k0 + i * kThreadsM;
+        if (key < k_end) {
+          old[i] = __ldcg(score + key);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (2 * j < a.s_rows) s[i][j] = __ldcg(reinterpret_cast<const float2*>(s_at + (size_t)key * a.s_rows) + j);
+        }
+      }
       // each row's maximum and the reciprocal of its sum, one warp a row
       __syncthreads();
       for (int row = warp; row < a.rows; row += kWarpsM) {
@@ -836,39 +889,48 @@ __global__ void __launch_bounds__(kThreadsM) kv4_attn_merge_kernel(const AttnArg
         const int c0 = line.cta_of(i0), c1 = line.cta_of(i0 + nb - 1);
         float m = -INFINITY, l = 0.f;
         if (c0 == c1) {
-          const float2 st = __ldcg(reinterpret_cast<const float2*>(a.stats) + ((size_t)seq * items + item) * R + rr);
+          const float2 st = __ldcg(a.stats + ((size_t)seq * items + item) * R + rr);
           m = st.x; l = st.y;
         } else {
-          for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, __ldcg(slot_of(i, c1) + R * D + rr));
-#pragma unroll
-          for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+#pragma unroll 2
           for (int i = c0 + lane; i <= c1; i += 32) {
             const float* p = slot_of(i, c1) + R * D + rr;
-            l = fmaf(rescale(__ldcg(p), m), __ldcg(p + R), l);
+            join(m, l, __ldcg(p), __ldcg(p + R));
           }
 #pragma unroll
-          for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
+          for (int o = 16; o; o >>= 1)
+            join(m, l, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, l, o));
         }
         // sums carry the bias of the probabilities
         if (lane == 0) stat[row] = make_float2(m == -INFINITY ? 0.f : kBias - m, l != 0.f ? 1.f / l : 0.f);
       }
       __syncthreads();
-      float* score = a.c.scores + ((size_t)seq * a.c.heads + kvh) * a.c.capacity();
-      for (int key = b0 * kKv4Block + tid; key < min(n, b1 * kKv4Block); key += kThreadsM) {
-        const float old = __ldcg(score + key);
+      auto weigh = [&](float w, float2 x, int row) {
+        if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
+        if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
+        return w;
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int key = k0 + i * kThreadsM;
+        if (key < k_end) {
+          float w = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (2 * j < a.s_rows) w = weigh(w, s[i][j], 2 * j);
+          score[key] = old[i] + w;
+        }
+      }
+      for (int key = k0 + kAhead * kThreadsM; key < k_end; key += kThreadsM) {
+        const float was = __ldcg(score + key);
         float w = 0.f;
         for (int tile = 0; tile < a.tiles; ++tile) {
-          const int unit = start + (tile * a.c.heads + kvh) * (nb + kStart) + kStart + key / kKv4Block;
-          const float* s = a.s_all + ((size_t)unit * kKv4Block + key % kKv4Block) * a.s_rows;
+          const float* p = s_at + ((size_t)tile * a.c.heads * (nb + kStart) * kKv4Block + key) * a.s_rows;
 #pragma unroll 4
-          for (int i = 0; i < a.s_rows; i += 2) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(s + i));
-            const int row = tile * R + i;
-            if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
-            if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
-          }
+          for (int i = 0; i < a.s_rows; i += 2)
+            w = weigh(w, __ldcg(reinterpret_cast<const float2*>(p + i)), tile * R + i);
         }
-        score[key] = old + w;
+        score[key] = was + w;
       }
     }
     v = stop;
@@ -882,7 +944,7 @@ __global__ void __launch_bounds__(kThreadsM) kv4_attn_merge_kernel(const AttnArg
 
 struct Layout {
   int R, tiles, s_rows;
-  size_t warp_part, cta_part, stats, s_all, bytes;   // byte offsets
+  size_t line, warp_part, cta_part, stats, s_all, bytes;   // byte offsets
 };
 
 // Query rows of a KV head: one tile of 8 columns up to 8, else tiles of 16
@@ -897,6 +959,7 @@ Layout layout_of(const mk_kv4_cache* c, int q_len, int group, bool accumulate) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t part = (size_t)l.R * (d + 2) * sizeof(float);
   size_t at = 0;
+  l.line = at; at = up(at + (1 + 2 * kMaxCtas) * sizeof(int4));
   l.warp_part = at; at = up(at + (size_t)kMaxCtas * kWarps * part);
   l.cta_part = at; at = up(at + (size_t)kMaxCtas * 2 * part);
   l.stats = l.s_all = at;
@@ -934,7 +997,8 @@ cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = pdl_launch(kv4_attn_kernel<D, DT, NT>, dim3(args.max_ctas), dim3(kThreadsA), smem, st, args);
   if (e != cudaSuccess) return e;
-  return pdl_launch(kv4_attn_merge_kernel<D, DT, 8 * NT>, dim3(args.max_ctas), dim3(kThreadsM), 0, st, args);
+  return pdl_launch(kv4_attn_merge_kernel<D, DT, 8 * NT>, dim3(args.max_ctas * (args.accumulate ? 2 : 1)),
+                    dim3(kThreadsM), 0, st, args);
 }
 
 template <int D, int DT>
@@ -998,7 +1062,10 @@ extern "C" int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, in
   a.accumulate = accumulate != 0;
   a.warp_part = reinterpret_cast<float*>(ws + l.warp_part);
   a.cta_part = reinterpret_cast<float*>(ws + l.cta_part);
-  a.stats = reinterpret_cast<float*>(ws + l.stats);
+  a.line = reinterpret_cast<int4*>(ws + l.line);
+  a.edges = a.line + 1;
+  a.begins = a.edges + kMaxCtas;
+  a.stats = reinterpret_cast<float2*>(ws + l.stats);
   a.s_all = reinterpret_cast<float*>(ws + l.s_all);
   a.s_rows = l.s_rows;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
