@@ -364,11 +364,10 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
     };
     uint32_t have = 0;   // bit i: the block i ahead of the current one has a page
     __syncwarp();        // the slots' last readers are done
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (b0 + i < b1 && issue()) have |= 1u << i;
-      cp_commit();
-    }
+    // one block each first: copies are served in order, so a warp's second block
+    // would hold up the first one of the warps behind it
+    if (issue()) have |= 1u;
+    cp_commit();
 
     uint32_t qf[QP][NT][2 * KS];
     float mul[NT][2];                // S -> log2 units, for this thread's columns 2t, 2t + 1
@@ -422,6 +421,11 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       see_all = min(see_all, lim[nt]);
     }
     see_all = __reduce_min_sync(0xFFFFFFFFu, see_all);
+#pragma unroll
+    for (int i = 1; i < kStages - 1; ++i) {
+      if (b0 + i < b1 && issue()) have |= 1u << i;
+      cp_commit();
+    }
 
     float o[NT][KS][4];
     float ref[NT][2], sum[NT][2];    // reference of the probabilities (log2 units), their sum
@@ -453,11 +457,12 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       float sc[2][NT][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        float s2[NT][4];   // two chains of products a half: an mma waits ~30 clocks for the one before
         const int ka = half * 16 + key_r, kb = ka + 8;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[half][nt][i] = 0.f;
+          for (int i = 0; i < 4; ++i) sc[half][nt][i] = s2[nt][i] = 0.f;
         uint32_t wa[KS / 2], wb[KS / 2];
         __half2 sa, sb;   // scales of this thread's two groups (d = 64: one)
         if (D == 128) {
@@ -489,9 +494,13 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma16816(sc[half][nt], ha[0], hb[0], ha[1], hb[1], qf[p][nt][4 * w], qf[p][nt][4 * w + 1]);
-              mma16816(sc[half][nt], ha[2], hb[2], ha[3], hb[3], qf[p][nt][4 * w + 2], qf[p][nt][4 * w + 3]);
+              mma16816(s2[nt], ha[2], hb[2], ha[3], hb[3], qf[p][nt][4 * w + 2], qf[p][nt][4 * w + 3]);
             }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[half][nt][i] += s2[nt][i];
       }
 
       if (masked) {
@@ -784,7 +793,7 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
 }
 
 template <int D, int DT, int R>
-__global__ void __launch_bounds__(kThreadsM) kv4_attn_merge_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const AttnArgs a) {
   __shared__ float2 stat[kMaxRows];
   pdl_trigger();
   pdl_wait();
