@@ -465,8 +465,7 @@ int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, int dtype, in
  * (-1 behind the last).  src is only read, so a prompt's pages may be shared;
  * dst has pages and scores of its own (same heads, head_dim, n_seq and log2;
  * page_tokens may differ), and its lens become min(lens, budget) by the
- * caller.  1 <= budget <= dst's capacity; keep_first + keep_last <= budget;
- * src's capacity below 2^21. */
+ * caller.  1 <= budget <= dst's capacity; keep_first + keep_last <= budget. */
 int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, int budget, int keep_first,
                  int keep_last, int32_t* kept_dev, void* stream);
 

@@ -188,25 +188,17 @@ __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs 
     a.sums[chunk] = make_float2(highest ? mx : -INFINITY, s);
   }
   if (found <= kFound) {
-    if (warp) return;
-    // each lane's share of the list, then W rounds
-    uint2 mine[kFound / 32];
-#pragma unroll
-    for (int i = 0; i < kFound / 32; ++i) {
-      mine[i] = make_uint2(0u, 0u);
-      if (i * 32 + lane < found) mine[i] = list[i * 32 + lane];
-    }
-    for (int j = 0; j < W; ++j) {
-      uint2 b = mine[0];
-#pragma unroll
-      for (int i = 1; i < kFound / 32; ++i)
-        if (mine[i].x > b.x || (mine[i].x == b.x && mine[i].y < b.y)) b = mine[i];
-      uint32_t k, i0;
-      warp_first(b.x, b.y, k, i0);
-      if (lane == 0) out[j] = make_uint2(k, k ? i0 : 0u);
-#pragma unroll
-      for (int i = 0; i < kFound / 32; ++i)
-        if (mine[i].x == k && mine[i].y == i0) mine[i].x = 0u;
+    // each one's rank by counting those before it
+    if ((int)threadIdx.x < found) {
+      const uint2 mine = list[threadIdx.x];
+      int rank = 0;
+      for (int j = 0; j < found; ++j) {
+        const uint2 o = list[j];
+        rank += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+      }
+      if (rank < W) out[rank] = mine;
+    } else if ((int)threadIdx.x < W) {
+      out[threadIdx.x] = make_uint2(0u, 0u);
     }
     return;
   }
@@ -263,10 +255,14 @@ __device__ __forceinline__ unsigned long long score_key64(double s) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-// HEADS: chunk heads of a lane.  WT: most beams; WT * WT / 32 candidates a lane.
+// One CTA a search, one warp a beam.  Every choice of the first W of a few is
+// made by rank: each candidate counts those before it, without a chain of
+// rounds.  HEADS: chunk heads of a lane.  WT: most beams.
 template <int HEADS, int WT>
 __global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) {
-  constexpr int kFinal = WT * WT < 32 ? 1 : WT * WT / 32;
+  constexpr int kOwn = WT * WT < 32 ? 1 : WT * WT / 32;   // candidates of a lane
+  __shared__ uint2 few[WT][HEADS * 32 > WT * WT ? HEADS * 32 : WT * WT];   // a beam's heads, then its lists
+  __shared__ int chosen[WT][WT];
   __shared__ unsigned long long cand_key[WT * WT];
   __shared__ double cand_score[WT * WT];
   __shared__ int32_t cand_token[WT * WT];
@@ -274,109 +270,122 @@ __global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) 
   pdl_wait();
   const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5, W = a.beams;
   const size_t row = (size_t)blockIdx.x * W + beam;
+  const float2* sums = a.sums + row * a.chunks;
+  const uint2* lists = a.lists + row * a.chunks * W;
+  // all in flight at once (a finished beam's are not written: not used)
   const double cum = __ldcg(a.cum + row);
   const bool finished = a.finished && __ldcg(a.finished + row);
+  float2 sum_of[HEADS];
+  uint2 head[HEADS];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int c = i * 32 + lane;
+    sum_of[i] = c < a.chunks ? __ldcg(sums + c) : make_float2(-INFINITY, 0.f);
+    head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
+  }
+  for (int j = lane; j < W; j += 32) {   // no candidates so far
+    cand_key[beam * W + j] = 0ull;
+    chosen[beam][j] = -1;
+  }
   if (finished) {
-    for (int j = lane; j < W; j += 32) {
-      const bool one = j == 0;
-      cand_key[beam * W + j] = one ? score_key64(cum) : 0ull;
-      cand_score[beam * W + j] = cum;
-      cand_token[beam * W + j] = a.eos;
+    if (lane == 0) {
+      cand_key[beam * W] = score_key64(cum);
+      cand_score[beam * W] = cum;
+      cand_token[beam * W] = a.eos;
     }
   } else {
-    // log-sum-exp over the chunks
-    const float2* sums = a.sums + row * a.chunks;
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) few[beam][i * 32 + lane] = head[i];
+    __syncwarp();
+    // the W chunks with the highest heads (a head's token tells ties apart)
+    const int live = min(a.chunks, HEADS * 32);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i)
+      if (head[i].x) {
+        int rank = 0;
+        for (int j = 0; j < live; ++j) {
+          const uint2 o = few[beam][j];
+          rank += o.x > head[i].x || (o.x == head[i].x && o.y < head[i].y);
+        }
+        if (rank < W) chosen[beam][rank] = i * 32 + lane;
+      }
+    __syncwarp();
+    // their lists, in flight during the log-sum-exp over all chunks
+    uint2 c[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int e = i * 32 + lane, from = e / W;
+      const int chunk = e < W * W ? chosen[beam][from] : -1;
+      c[i] = chunk >= 0 ? __ldcg(lists + (size_t)chunk * W + (e - from * W)) : make_uint2(0u, 0u);
+    }
     float mx = -INFINITY;
-    for (int c = lane; c < a.chunks; c += 32) mx = fmaxf(mx, __ldcg(sums + c).x);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) mx = fmaxf(mx, sum_of[i].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     double sum = 0.0;
-    for (int c = lane; c < a.chunks; c += 32) {
-      const float2 s = __ldcg(sums + c);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i)
       // a chunk without a candidate has maximum -inf and adds its sum: 0, or a NaN
-      sum += s.x > -INFINITY ? (double)s.y * exp((double)s.x - (double)mx) : (double)s.y;
-    }
+      sum += sum_of[i].x > -INFINITY ? (double)sum_of[i].y * exp((double)sum_of[i].x - (double)mx) : (double)sum_of[i].y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     const double lse = (double)mx + log(sum);
-    // the W chunks with the highest heads
-    const uint2* lists = a.lists + row * a.chunks * W;
-    uint2 head[HEADS];
+    // the beam's W best of W * W
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      const int c = i * 32 + lane;
-      head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
-    }
-    int chosen = -1;   // lane j: the j-th of them
-    for (int j = 0; j < W; ++j) {
-      uint32_t mine = 0, tok = 0xFFFFFFFFu;
+    for (int i = 0; i < kOwn; ++i)
+      if (i * 32 + lane < W * W) few[beam][i * 32 + lane] = c[i];
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < HEADS; ++i)
-        if (head[i].x > mine) { mine = head[i].x; tok = head[i].y; }   // chunks grow with i
-      uint32_t k, t;
-      warp_first(mine, tok, k, t);
-      if (k == 0u) break;
-      if (lane == j) chosen = (int)t / kChunk;
-#pragma unroll
-      for (int i = 0; i < HEADS; ++i)
-        if (head[i].x == k && head[i].y == t) head[i].x = 0u;
-    }
-    // their lists: W * W keys, a lane's share in registers
-    uint2 c[kFinal];
-#pragma unroll
-    for (int i = 0; i < kFinal; ++i) {
-      const int e = i * 32 + lane, from = e / W;
-      const int chunk = __shfl_sync(0xFFFFFFFFu, chosen, from & 31);
-      c[i] = e < W * W && chunk >= 0 ? __ldcg(lists + (size_t)chunk * W + (e - from * W)) : make_uint2(0u, 0u);
-    }
-    for (int j = 0; j < W; ++j) {
-      uint32_t mine = 0, tok = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = 0; i < kFinal; ++i)
-        if (c[i].x > mine || (c[i].x == mine && mine && c[i].y < tok)) { mine = c[i].x; tok = c[i].y; }
-      uint32_t k, t;
-      warp_first(mine, tok, k, t);
-#pragma unroll
-      for (int i = 0; i < kFinal; ++i)
-        if (c[i].x == k && c[i].y == t) c[i].x = 0u;
-      if (lane == 0) {
-        const double s = k ? cum + ((double)key_logit(k) - lse) : -INFINITY;
-        cand_key[beam * W + j] = score_key64(s);
-        cand_score[beam * W + j] = s;
-        cand_token[beam * W + j] = (int32_t)t;
+    for (int i = 0; i < kOwn; ++i)
+      if (c[i].x) {
+        int rank = 0;
+        for (int j = 0; j < W * W; ++j) {
+          const uint2 o = few[beam][j];
+          rank += o.x > c[i].x || (o.x == c[i].x && o.y < c[i].y);
+        }
+        if (rank < W) {
+          const double s = cum + ((double)key_logit(c[i].x) - lse);
+          cand_key[beam * W + rank] = score_key64(s);
+          cand_score[beam * W + rank] = s;
+          cand_token[beam * W + rank] = (int32_t)c[i].y;
+        }
       }
-    }
   }
   __syncthreads();
-  if (beam) return;
-  // the W first of W * W: highest score, then lowest beam, then the beam's own order
-  unsigned long long key[kFinal];
-#pragma unroll
-  for (int i = 0; i < kFinal; ++i) key[i] = i * 32 + lane < W * W ? cand_key[i * 32 + lane] : 0ull;
-  for (int j = 0; j < W; ++j) {
-    unsigned long long mine = 0;
-    uint32_t idx = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < kFinal; ++i)
-      if (key[i] > mine) { mine = key[i]; idx = i * 32 + lane; }
-    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(mine >> 32));
-    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
-    const unsigned long long k = (unsigned long long)hi << 32 | lo;
-    const uint32_t who = __reduce_min_sync(0xFFFFFFFFu, mine == k ? idx : 0xFFFFFFFFu);
-#pragma unroll
-    for (int i = 0; i < kFinal; ++i)
-      if (i * 32 + lane == (int)who) key[i] = 0ull;
-    if (lane == 0) {
-      const size_t to = (size_t)blockIdx.x * W + j;
-      // fewer candidates than beams: a dead one, which keeps its own state
-      const int parent = k ? (int)who / W : j, token = k ? cand_token[who] : max(a.eos, 0);
+  // the W first of W * W: highest score, then lowest beam, then the beam's own
+  // order; a dead beam, which keeps its own state, behind the last candidate
+  int live = 0;
+  for (int e = threadIdx.x; e < W * W; e += 32 * W) {
+    const unsigned long long k = cand_key[e];
+    int rank = 0;
+    live = 0;
+    for (int j = 0; j < W * W; ++j) {
+      const unsigned long long o = cand_key[j];
+      rank += o > k || (o == k && j < e);
+      live += o != 0ull;
+    }
+    const bool real = k != 0ull;
+    if (real && rank < W) {
+      const size_t to = (size_t)blockIdx.x * W + rank;
+      const int parent = e / W, token = cand_token[e];
       a.tokens[to] = token;
       a.parents[to] = parent;
-      a.scores[to] = k ? (float)cand_score[who] : -INFINITY;
+      a.scores[to] = (float)cand_score[e];
       if (a.done)
         a.done[to] = (a.finished && __ldcg(a.finished + (size_t)blockIdx.x * W + parent)) ||
                      (a.eos >= 0 && token == a.eos);
     }
+  }
+  // threads 0 .. W - 1 have counted the live ones (W <= W * W)
+  if ((int)threadIdx.x < W && (int)threadIdx.x >= live) {
+    const int j = threadIdx.x;
+    const size_t to = (size_t)blockIdx.x * W + j;
+    a.tokens[to] = max(a.eos, 0);
+    a.parents[to] = j;
+    a.scores[to] = -INFINITY;
+    if (a.done) a.done[to] = (a.finished && __ldcg(a.finished + to)) || a.eos >= 0;
   }
 }
 

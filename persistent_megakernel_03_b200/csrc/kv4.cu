@@ -53,32 +53,28 @@ Kv4 kv4_of(const mk_kv4_cache* c) {
 
 // ------------------------------------------------------------------ append
 
-__device__ __forceinline__ void load16(const void* p, int dtype, float (&x)[16]) {
+// 16 input elements, raw, as fp32.
+__device__ __forceinline__ void widen_input(const uint4 (&raw)[4], int dtype, float (&x)[16]) {
   if (dtype == MK_DTYPE_F32) {
-    const float4* f = static_cast<const float4*>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldcg(f + i);
-      x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      x[4 * i] = __uint_as_float(raw[i].x); x[4 * i + 1] = __uint_as_float(raw[i].y);
+      x[4 * i + 2] = __uint_as_float(raw[i].z); x[4 * i + 3] = __uint_as_float(raw[i].w);
     }
     return;
   }
-  const uint4* u = static_cast<const uint4*>(p);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldcg(u + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float a, b;
       if (dtype == MK_DTYPE_BF16) {
-        a = __uint_as_float(w[j] << 16);
-        b = __uint_as_float(w[j] & 0xFFFF0000u);
+        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
       } else {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        a = f.x; b = f.y;
+        x[8 * i + 2 * j] = f.x; x[8 * i + 2 * j + 1] = f.y;
       }
-      x[8 * i + 2 * j] = a; x[8 * i + 2 * j + 1] = b;
     }
   }
 }
@@ -144,56 +140,78 @@ constexpr int kAppendSmemSeq = 512;   // offsets kept in shared memory up to thi
 // One thread per 16 dims of one token's key and value (one KV head).  The
 // input is read once and 9 bytes written for its 32 or 64; threads of a warp
 // hold consecutive groups of the token, so reads are contiguous and a row's
-// codes are written as whole 32-byte sectors.
+// codes are written as whole 32-byte sectors.  One wave of CTAs goes over the
+// tokens: where a token goes takes three dependent loads (offsets, length,
+// page), of which a CTA makes the first two once, and each thread's next
+// input is in flight while it rounds the current one.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 3)
     kv4_append_kernel(Kv4 c, const uint8_t* k, const uint8_t* v, int dtype, size_t k_stride, size_t v_stride,
                       const int32_t* offsets, int n_tokens, int k_neg, int v_neg) {
   using S = Kv4Shape<D>;
-  __shared__ int32_t offs[kAppendSmemSeq + 1];
+  __shared__ int32_t offs[kAppendSmemSeq + 1], lens[kAppendSmemSeq];
   pdl_trigger();
   pdl_wait();
+  constexpr int G = D / kKv4Group;
+  const uint32_t per = c.heads * G, total = per * (uint32_t)n_tokens;   // threads of a token, of the call
+  const uint32_t step = gridDim.x * kAppendThreads;
+  uint32_t id = blockIdx.x * kAppendThreads + threadIdx.x;
+  const int esz = dtype == MK_DTYPE_F32 ? 4 : 2;
+  uint4 raw[2][4];
+  auto fetch = [&](uint32_t i) {
+    if (i >= total) return;
+    const uint32_t tok = i / per;
+    const size_t at = (size_t)(i - tok * per) * kKv4Group * esz;
+    const uint4* a = reinterpret_cast<const uint4*>(k + (size_t)tok * k_stride + at);
+    const uint4* b = reinterpret_cast<const uint4*>(v + (size_t)tok * v_stride + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < 2 || esz == 4) { raw[0][j] = __ldcg(a + j); raw[1][j] = __ldcg(b + j); }
+  };
+  fetch(id);
   const bool near = c.n_seq <= kAppendSmemSeq;
   if (near) {
-    for (int i = threadIdx.x; i <= c.n_seq; i += kAppendThreads) offs[i] = __ldcg(offsets + i);
+    for (int i = threadIdx.x; i <= c.n_seq; i += kAppendThreads) {
+      offs[i] = __ldcg(offsets + i);
+      if (i < c.n_seq) lens[i] = __ldcg(c.lens + i);
+    }
     __syncthreads();
   }
-  constexpr int G = D / kKv4Group;
-  const uint32_t per = c.heads * G;   // threads of a token
-  const uint32_t id = blockIdx.x * kAppendThreads + threadIdx.x;
-  const int tok = (int)(id / per);
-  if (tok >= n_tokens) return;
-  const uint32_t part = id - tok * per;
-  const int head = part / G, g = part % G;
-  // the input does not depend on where it goes: in flight during the search
-  const size_t at_dim = (size_t)(head * D + g * kKv4Group) * (dtype == MK_DTYPE_F32 ? 4 : 2);
-  float x[2][16];
-  load16(k + (size_t)tok * k_stride + at_dim, dtype, x[0]);
-  load16(v + (size_t)tok * v_stride + at_dim, dtype, x[1]);
   auto at = [&](int i) { return near ? offs[i] : __ldcg(offsets + i); };
-  int lo = 0, hi = c.n_seq - 1;   // the last sequence whose offset is <= tok
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (at(mid) <= tok) lo = mid; else hi = mid - 1;
-  }
-  const int first = at(lo), end = at(lo + 1);
-  if (tok < first || tok >= end) return;   // before the first sequence or behind the last
-  const long long slot = (long long)__ldcg(c.lens + lo) - end + tok;
-  if (slot < 0 || slot >= c.capacity()) return;
-  const int lp = (int)slot / c.page_tokens, in = (int)slot - lp * c.page_tokens;
-  const int page = c.page(lo, lp);
-  if (page < 0) return;
-  uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
-  const int row = in % kKv4Block;
+  for (; id < total; id += step) {
+    const int tok = (int)(id / per);
+    const uint32_t part = id - tok * per;
+    const int head = part / G, g = part % G;
+    int lo = 0, hi = c.n_seq - 1;   // the last sequence whose offset is <= tok
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at(mid) <= tok) lo = mid; else hi = mid - 1;
+    }
+    const int first = at(lo), end = at(lo + 1);
+    const long long slot = (long long)(near ? lens[lo] : __ldcg(c.lens + lo)) - end + tok;
+    // tokens before the first sequence or behind the last, slots out of range: nothing
+    const bool ok = tok >= first && tok < end && slot >= 0 && slot < c.capacity();
+    const int lp = ok ? (int)slot / c.page_tokens : 0, in = (int)slot - lp * c.page_tokens;
+    const int page = ok ? c.page(lo, lp) : -1;
+    uint2 codes[2];
+    uint32_t scale[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint2 codes;
-    uint32_t scale;
-    quantize16(x[i], i ? v_neg : k_neg, codes, scale);
-    *reinterpret_cast<uint2*>(b + (i ? S::kVc : 0) + row * S::kCodes + g * 8) = codes;
-    b[(i ? S::kVs : S::kKs) + row * S::kScales + g] = (uint8_t)scale;
+    for (int i = 0; i < 2; ++i) {
+      float x[16];
+      widen_input(raw[i], dtype, x);
+      quantize16(x, i ? v_neg : k_neg, codes[i], scale[i]);
+    }
+    fetch(id + step);
+    if (page < 0) continue;
+    uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
+    const int row = in % kKv4Block;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<uint2*>(b + (i ? S::kVc : 0) + row * S::kCodes + g * 8) = codes[i];
+      b[(i ? S::kVs : S::kKs) + row * S::kScales + g] = (uint8_t)scale[i];
+    }
+    if (c.scores && g == 0) c.scores[((size_t)lo * c.heads + head) * c.capacity() + slot] = 0.f;
   }
-  if (c.scores && g == 0) c.scores[((size_t)lo * c.heads + head) * c.capacity() + slot] = 0.f;
 }
 
 // -------------------------------------------------------------------- read
@@ -249,10 +267,9 @@ __global__ void __launch_bounds__(kReadThreads)
   const int g = threadIdx.x % G;
   const int slot = blockIdx.x * kRows + threadIdx.x / G;
   const int head = blockIdx.y, s = blockIdx.z;
-  if (slot >= n || slot >= c.len(s)) return;
-  const int lp = slot / c.page_tokens, in = slot - lp * c.page_tokens;
-  const int page = c.page(s, lp);
-  if (page < 0) return;
+  const int lp = min(slot, c.capacity() - 1) / c.page_tokens, in = slot - lp * c.page_tokens;
+  const int len = c.len(s), page = c.page(s, lp);   // both in flight
+  if (slot >= n || slot >= len || page < 0) return;
   const uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
   const int row = in % kKv4Block;
   const uint2 kc = *reinterpret_cast<const uint2*>(b + row * S::kCodes + g * 8);
@@ -289,72 +306,36 @@ __device__ __forceinline__ void store_peer(void* mine, int rank, unsigned long l
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(b), "l"(v) : "memory");
 }
 
-// Sums over a head's CTAs of three counts below 2^21 each, in 21 bits of 64.
-// Rows that calls alternate between, so that a fast warp's or CTA's next
-// numbers do not meet a slow one's reading.
-struct SelShared {
-  unsigned long long warp[2][kSelWarps];
-  unsigned long long cta[2][kSelCtas];
-};
-__device__ __forceinline__ unsigned long long three(uint32_t a, uint32_t b, uint32_t c) {
-  return (unsigned long long)a | (unsigned long long)b << 21 | (unsigned long long)c << 42;
-}
-__device__ __forceinline__ uint32_t one_of(unsigned long long v, int i) { return (uint32_t)(v >> (21 * i)) & 0x1FFFFFu; }
-__device__ __forceinline__ unsigned long long warp_three(unsigned long long v) {
-  return three(__reduce_add_sync(0xFFFFFFFFu, one_of(v, 0)), __reduce_add_sync(0xFFFFFFFFu, one_of(v, 1)),
-               __reduce_add_sync(0xFFFFFFFFu, one_of(v, 2)));
-}
-
-// `v`: this warp's counts.  Every thread of the cluster gets the sum of all,
-// and that of the CTAs before its own.
-__device__ __forceinline__ unsigned long long sum_all(unsigned long long v, SelShared& s, int& flip, int rank,
-                                                      int ctas, unsigned long long* before = nullptr) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) s.warp[flip][warp] = v;
-  __syncthreads();
-  unsigned long long all = 0ull, low = 0ull;
-  if (ctas == 1) {
-    all = warp_three(s.warp[flip][lane]);
-  } else {
-    if (warp == 0) {
-      const unsigned long long t = warp_three(s.warp[flip][lane]);
-      if (lane < ctas) store_peer(&s.cta[flip][rank], lane, t);
-    }
-    cluster_arrive();
-    cluster_wait();
-    for (int i = 0; i < ctas; ++i) {
-      const unsigned long long t = s.cta[flip][i];
-      all += t;
-      if (i < rank) low += t;
-    }
-  }
-  if (before) *before = low;
-  flip ^= 1;
-  return all;
+__device__ __forceinline__ uint32_t load_peer(const void* mine, int rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), b, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(b) : "memory");
+  return v;
 }
 
 // Which slots a head keeps: the `take` highest scores between the protected
 // ends.  A head's keys are cut into contiguous parts, one for each CTA of a
 // cluster, and stay in registers (KPT a thread; longer parts are read from L2
-// again for each step).  The threshold -- the highest T with at least `take` keys
-// >= T -- is found two bits at a time from the top: one pass counts the keys
-// above three candidates, three 21-bit counters in a 64-bit sum, over the
-// cluster's shared memory.  A count is bound by the integer pipe (3
-// instructions a key and candidate, 64 lanes a clock and SM: 32,768 keys on
-// one SM took 47 us), so it pays to spread a head; each step costs ~600 clocks
-// of barriers, so two bits a step beat one (half the steps) and three (seven
-// candidates for three bits).  A histogram per digit would need fewer passes,
-// but accumulated weights share their exponents, so its shared-memory adds run
-// one after another on a few bins.  The search stops at the first T with
-// exactly `take` keys above.  Slots above T, and the lowest of those on it, are
-// then written in slot order by prefix sums:
-// position = (# above before) + min(# equal before, equals wanted).
+// again for each digit).  The threshold -- the `take`-th highest key -- is found
+// a digit of 8 bits at a time from the top: a histogram of the keys that
+// share the digits so far in each CTA's shared memory, summed over the
+// cluster's.  Accumulated weights share their exponents, so the first digit's
+// adds meet on few bins (~10 of a warp's 32 lanes on one); that still costs
+// less than counting keys above candidate thresholds bit by bit, which the
+// integer pipe bounds: 8 heads of 32,768 keys, one bit a step on one SM each 47
+// us, two bits a step over 8 SMs 21 us, digits ~9 us.  A warp whose keys all
+// have one digit (scores that are all equal) adds them once.  Slots above the threshold,
+// and the lowest of those on it, are then written in slot order by prefix
+// sums: position = (# above before) + min(# equal before, equals wanted).
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads, 1)
     kv4_select_kernel(Kv4 c, int budget, int first, int last, int ctas, int32_t* kept) {
-  __shared__ SelShared sh;
-  __shared__ uint32_t cnt[KPT][kSelWarps], sums[kSelWarps];
+  __shared__ uint32_t hist[4][256];    // a digit each: no CTA clears one that another still reads
+  __shared__ uint32_t cnt[KPT][kSelWarps], sums[kSelWarps], above_warp[8];
+  __shared__ uint32_t digit_found, above_found, here_found;
+  __shared__ unsigned long long by_cta[kSelCtas];
   pdl_trigger();
+  for (int i = threadIdx.x; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0u;
   pdl_wait();
   const int rank = ctas > 1 ? blockIdx.x % ctas : 0, head = blockIdx.x / ctas, s = blockIdx.y, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
@@ -369,7 +350,6 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   for (int i = from; i < first; i += step) out[i] = i;
   for (int i = from; i < last; i += step) out[budget - last + i] = n - last + i;
   if (take == 0) return;
-  if (ctas > 1) cluster_arrive();   // every CTA has begun before another writes its shared memory
   // this CTA's part
   const int part = (m_all + ctas - 1) / ctas, p0 = min(m_all, rank * part), m = min(m_all, p0 + part) - p0;
   const float* sc = c.scores + ((size_t)s * c.heads + head) * c.capacity() + first + p0;
@@ -380,55 +360,100 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     const int i = j * kSelThreads + tid;
     key[j] = whole && i < m ? score_key(__ldcg(sc + i)) : 0u;
   }
-  if (ctas > 1) cluster_wait();
-  int flip = 0;
-  // keys >= a, b, c in 21 bits each, a <= b <= c; a > 0, so the padding zeros never count
-  auto at_least = [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-    if (whole) {   // three counts of at most 512 a warp in one word
-      uint32_t v = 0;
+  __syncthreads();   // the histograms are clear
+
+  uint32_t T = 0, want = (uint32_t)take;   // digits so far; the threshold's rank among the keys that have them
+  bool exact = false;                      // all keys with these digits are kept: none is on a border
+  int shift = 32;
+#pragma unroll 1
+  for (int d = 0; d < 4 && !exact; ++d) {
+    shift -= 8;
+    auto add = [&](uint32_t k, bool in) {
+      in = in && (d == 0 || k >> (shift + 8) == T >> (shift + 8));
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
+      if (mask == 0u) return;
+      const uint32_t b = k >> shift & 255u, b0 = __shfl_sync(0xFFFFFFFFu, b, __ffs(mask) - 1);
+      if (__all_sync(0xFFFFFFFFu, !in || b == b0)) {
+        if (lane == 0) atomicAdd(&hist[d][b0], (uint32_t)__popc(mask));
+      } else if (in) {
+        atomicAdd(&hist[d][b], 1u);
+      }
+    };
+    if (whole) {
 #pragma unroll
-      for (int j = 0; j < KPT; ++j)
-        v += (key[j] >= t1 ? 1u : 0u) + (key[j] >= t2 ? 1u << 10 : 0u) + (key[j] >= t3 ? 1u << 20 : 0u);
-      v = __reduce_add_sync(0xFFFFFFFFu, v);
-      return sum_all(three(v & 1023u, v >> 10 & 1023u, v >> 20), sh, flip, rank, ctas);
+      for (int j = 0; j < KPT; ++j) add(key[j], j * kSelThreads + tid < m);
+    } else {
+      for (int i = tid; i < ((m + 31) & ~31); i += kSelThreads) add(i < m ? score_key(__ldcg(sc + i)) : 0u, i < m);
     }
-    uint32_t v1 = 0, v2 = 0, v3 = 0;
-    for (int i = tid; i < m; i += kSelThreads) {
-      const uint32_t k = score_key(__ldcg(sc + i));
-      v1 += k >= t1; v2 += k >= t2; v3 += k >= t3;
-    }
-    return sum_all(warp_three(three(v1, v2, v3)), sh, flip, rank, ctas);
-  };
-  uint32_t T = 0, have = (uint32_t)m_all;
-  for (int bit = 30; bit >= 0 && have != (uint32_t)take; bit -= 2) {
-    const unsigned long long a = at_least(T | 1u << bit, T | 2u << bit, T | 3u << bit);
+    if (ctas > 1) { cluster_arrive(); cluster_wait(); }
+    else __syncthreads();
+    uint32_t mine = 0, inc = 0;
+    if (tid < 256) {   // a thread a bin, the highest first
+      const int bin = 255 - tid;
+      if (ctas > 1) {
+        for (int i = 0; i < ctas; ++i) mine += load_peer(&hist[d][bin], i);
+      } else {
+        mine = hist[d][bin];
+      }
+      inc = mine;
 #pragma unroll
-    for (int k = 2; k >= 0; --k)
-      if (one_of(a, k) >= (uint32_t)take) { T |= (uint32_t)(k + 1) << bit; have = one_of(a, k); break; }
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) above_warp[warp] = inc;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      for (int w = 0; w < warp; ++w) inc += above_warp[w];
+      if (inc >= want && inc - mine < want) {
+        digit_found = 255 - tid;
+        above_found = inc - mine;
+        here_found = mine;
+      }
+    }
+    __syncthreads();
+    T |= digit_found << shift;
+    want -= above_found;
+    exact = here_found == want;
   }
-  // `have` keys are >= T.  Exactly `take`: all of them are kept and none is on
-  // the border; otherwise T is a key's value and the lowest slots on it fill up.
-  const bool exact = have == (uint32_t)take;
-  auto above = [&](uint32_t k) { return exact ? k >= T : k > T; };
-  uint32_t gt = 0, eq = 0;
-  if (whole) {
+  // `want` of the keys with T's digits are kept besides all above them
+  auto is_gt = [&](uint32_t k) { return exact ? k >= T : k > T; };
+  auto is_eq = [&](uint32_t k) { return !exact && k == T; };
+  uint32_t base_gt = 0, base_eq = 0;   // in the CTAs before
+  const uint32_t equals = exact ? 0u : want;
+  if (ctas > 1) {
+    uint32_t gt = 0, eq = 0;
+    if (whole) {
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
-      const bool in = j * kSelThreads + tid < m;
-      gt += in && above(key[j]);
-      eq += in && !exact && key[j] == T;
+      for (int j = 0; j < KPT; ++j) {
+        const bool in = j * kSelThreads + tid < m;
+        gt += in && is_gt(key[j]);
+        eq += in && is_eq(key[j]);
+      }
+    } else {
+      for (int i = tid; i < m; i += kSelThreads) {
+        const uint32_t k = score_key(__ldcg(sc + i));
+        gt += is_gt(k);
+        eq += is_eq(k);
+      }
     }
-  } else {
-    for (int i = tid; i < m; i += kSelThreads) {
-      const uint32_t k = score_key(__ldcg(sc + i));
-      gt += above(k);
-      eq += !exact && k == T;
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    if (lane == 0) { cnt[0][warp] = gt; sums[warp] = eq; }
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned long long t = (unsigned long long)__reduce_add_sync(0xFFFFFFFFu, cnt[0][lane]) |
+                                   (unsigned long long)__reduce_add_sync(0xFFFFFFFFu, sums[lane]) << 32;
+      if (lane < ctas) store_peer(&by_cta[rank], lane, t);
+    }
+    cluster_arrive();   // also: no CTA leaves while another reads its histograms
+    cluster_wait();
+    for (int i = 0; i < rank; ++i) {
+      base_gt += (uint32_t)by_cta[i];
+      base_eq += (uint32_t)(by_cta[i] >> 32);
     }
   }
-  unsigned long long low;
-  const unsigned long long sum = sum_all(warp_three(three(gt, eq, 0u)), sh, flip, rank, ctas, &low);
-  uint32_t base_gt = one_of(low, 0), base_eq = one_of(low, 1);   // in the CTAs before
-  const uint32_t equals = (uint32_t)take - one_of(sum, 0);
   for (int base = 0; base < m; base += KPT * kSelThreads) {
     if (!whole) {
 #pragma unroll
@@ -441,7 +466,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
       const bool in = base + j * kSelThreads + tid < m;
-      const bool g = in && above(key[j]), e = in && !exact && key[j] == T;
+      const bool g = in && is_gt(key[j]), e = in && is_eq(key[j]);
       g_bits |= (uint32_t)g << j;
       e_bits |= (uint32_t)e << j;
       const uint32_t bg = __ballot_sync(0xFFFFFFFFu, g), be = __ballot_sync(0xFFFFFFFFu, e);
@@ -566,8 +591,13 @@ extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const
     return kv4_fail(MK_ERR_INVALID_ARG, who, "keys and values of a token are 16-byte aligned");
   const Kv4 c = kv4_of(cache);
   const long long threads = (long long)n_tokens * c.heads * (cache->head_dim / kKv4Group);
-  const long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
-  if (threads > 0x7FFFFFFFll) return kv4_fail(MK_ERR_INVALID_ARG, who, "too many tokens in one call");
+  long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return kv4_fail(MK_ERR_CUDA, who, "no device");
+  if (blocks > 3ll * sms) blocks = 3ll * sms;
+  if (threads > 0x7FFFFFFFll - 1024 * kAppendThreads) return kv4_fail(MK_ERR_INVALID_ARG, who, "too many tokens in one call");
   const uint8_t* k = static_cast<const uint8_t*>(k_dev);
   const uint8_t* v = static_cast<const uint8_t*>(v_dev);
   const size_t ks = (size_t)k_stride * esz, vs = (size_t)v_stride * esz;
@@ -610,8 +640,6 @@ extern "C" int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, in
   if (!src->scores_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "the source has scores");
   if (budget < 1 || budget > (long long)dst->pages_per_seq * dst->page_tokens)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "budget is 1 to the destination's capacity");
-  if ((long long)src->pages_per_seq * src->page_tokens > (1 << 21) - 1)
-    return kv4_fail(MK_ERR_UNSUPPORTED, who, "a sequence of the source holds fewer than 2^21 keys");
   if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > budget)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "keep_first + keep_last is 0 to budget");
   if (!kept_dev || (reinterpret_cast<uintptr_t>(kept_dev) & 3u))
