@@ -54,7 +54,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreadsA = kWarps * 32;
-constexpr int kStages = 3;        // blocks of a warp's ring
+constexpr int kStages = 2;        // blocks of a warp's ring: one loads while the other is used
 constexpr int kMaxCtas = 320;     // partials are laid out for this many CTAs
 constexpr int kMaxRows = 1024;    // query rows of a KV head: q_len * group
 // Probabilities are 2^(S - ref + kBias), S at most kSlack above the reference:
@@ -109,7 +109,6 @@ struct AttnArgs {
   int32_t max_ctas;
   int32_t accumulate;
   // workspace
-  float* warp_part;      // [max_ctas * kWarps][R][d + 2]: a warp's first, unfinished piece
   float* cta_part;       // [max_ctas][2][R][d + 2]: a CTA's first and last, unfinished
   float2* stats;         // [n_seq * tiles * heads][R]: max and sum of rows that one CTA finished
   float* s_all;          // [units][32][stored rows]: scores in log2 units
@@ -251,6 +250,18 @@ __device__ __forceinline__ __half2 scales2(uint32_t two) {
   return *reinterpret_cast<const __half2*>(&h);
 }
 
+// Shared memory of a warp: the ring and behind it the query fragments (more than
+// one 8-row tile), which a last piece may overwrite; a first piece.
+template <int D, int DT, int NT>
+struct AttnSmem {
+  static constexpr int kRing = kStages * Kv4Shape<D>::kBytes;
+  static constexpr int kQ = NT > 1 ? (DT == MK_DTYPE_F32 ? 2 : 1) * NT * (D / 32) * 512 : 0;
+  static constexpr int kPiece = 8 * NT * D * 4;
+  static constexpr int kFirst = kRing + kQ > kPiece ? kRing + kQ : kPiece;
+  static constexpr int kWarp = kFirst + kPiece;
+  static constexpr int kBytes = kWarps * kWarp;
+};
+
 // D: head dim.  DT: MK_DTYPE_* of queries and outputs.  NT: 8-row tiles of query rows.
 template <int D, int DT, int NT>
 __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(const AttnArgs a) {
@@ -259,10 +270,12 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   constexpr int QP = DT == MK_DTYPE_F32 ? 2 : 1;   // fp16 parts of a query
   constexpr int PP = DT == MK_DTYPE_BF16 ? 1 : 2;  // and of a probability
   constexpr int KS = D / 16;                       // contraction steps, and 16-dim tiles of O
-  constexpr int kPart = R * (D + 2);
-  static_assert(kPart * 4 <= kStages * S::kBytes, "a warp's last piece takes the place of its ring");
+  using M = AttnSmem<D, DT, NT>;
+  // Query fragments: registers for one row tile; for more, shared memory, which both
+  // halves of a block read them from once
+  constexpr bool kQShared = NT > 1;
   extern __shared__ __align__(16) uint8_t ring_all[];
-  // pieces that a warp leaves: even its first, in global memory, odd its last, in its ring's place
+  // pieces that a warp leaves: even its first, in a place of its own, odd its last, in its ring's
   __shared__ int4 piece_of[2 * kWarps];    // sequence, item (-1: none), first block's unit, blocks
   __shared__ float piece_max[2 * kWarps][R], piece_sum[2 * kWarps][R];
   __shared__ float weight[kWarps][R], total[R];
@@ -293,7 +306,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   if (u < u_end) line_find(a, scan, u, seq, start, n);
   if (lane < 2) piece_of[2 * warp + lane] = make_int4(0, -1, 0, 0);
 
-  uint8_t* ring = ring_all + (size_t)warp * kStages * S::kBytes;
+  uint8_t* ring = ring_all + warp * M::kWarp;
+  uint4* q_shared = reinterpret_cast<uint4*>(ring + M::kRing) + lane;
   const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const int per = a.c.page_tokens / kKv4Block;
 
@@ -369,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
     if (issue()) have |= 1u;
     cp_commit();
 
-    uint32_t qf[QP][NT][2 * KS];
+    uint32_t qf[QP][kQShared ? 1 : NT][2 * KS];
     float mul[NT][2];                // S -> log2 units, for this thread's columns 2t, 2t + 1
     int limit[NT][2];                // keys those columns see
     int see_all = this_n;            // keys that every row sees
@@ -407,11 +421,19 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       for (int i = 0; i < 2 * KS; ++i) {
         const float f0 = x[2 * i] * up, f1 = x[2 * i + 1] * up;
         const uint32_t h = pack_half2(f0, f1);
-        qf[0][nt][i] = h;
+        qf[0][kQShared ? 0 : nt][i] = h;
         if (QP == 2) {
           const float2 b = unpack_half2(h);
-          qf[QP - 1][nt][i] = pack_half2(f0 - b.x, f1 - b.y);
+          qf[QP - 1][kQShared ? 0 : nt][i] = pack_half2(f0 - b.x, f1 - b.y);
         }
+      }
+      if (kQShared) {
+#pragma unroll
+        for (int p = 0; p < QP; ++p)
+#pragma unroll
+          for (int w = 0; w < KS / 2; ++w)
+            q_shared[((p * NT + nt) * (KS / 2) + w) * 32] =
+                make_uint4(qf[p][0][4 * w], qf[p][0][4 * w + 1], qf[p][0][4 * w + 2], qf[p][0][4 * w + 3]);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -453,54 +475,63 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       have >>= 1;
       const bool masked = !there || (b + 1) * kKv4Block > see_all;   // some row does not see some key
 
-      // S^T, 16 keys at a time
+      // S^T: 16 keys (a half) are an mma's rows; a word holds 8 of a key's dims
       float sc[2][NT][4];
+      {
+        uint32_t wa[2][KS / 2], wb[2][KS / 2];   // keys of mma rows r and r + 8
+        __half2 sa[2], sb[2];   // scales of this thread's two groups (d = 64: one)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float s2[NT][4];   // two chains of products a half: an mma waits ~30 clocks for the one before
-        const int ka = half * 16 + key_r, kb = ka + 8;
+        for (int half = 0; half < 2; ++half) {
+          const int ka = half * 16 + key_r, kb = ka + 8;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[half][nt][i] = s2[nt][i] = 0.f;
-        uint32_t wa[KS / 2], wb[KS / 2];
-        __half2 sa, sb;   // scales of this thread's two groups (d = 64: one)
-        if (D == 128) {
-          const uint4 va = *reinterpret_cast<const uint4*>(blk + ka * S::kCodes + t * 16);
-          const uint4 vb = *reinterpret_cast<const uint4*>(blk + kb * S::kCodes + t * 16);
-          wa[0] = va.x; wa[1] = va.y; wa[KS / 2 - 2] = va.z; wa[KS / 2 - 1] = va.w;
-          wb[0] = vb.x; wb[1] = vb.y; wb[KS / 2 - 2] = vb.z; wb[KS / 2 - 1] = vb.w;
-          sa = scales2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + ka * S::kScales + 2 * t));
-          sb = scales2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + kb * S::kScales + 2 * t));
-        } else {
-          const uint2 va = *reinterpret_cast<const uint2*>(blk + ka * S::kCodes + t * 8);
-          const uint2 vb = *reinterpret_cast<const uint2*>(blk + kb * S::kCodes + t * 8);
-          wa[0] = va.x; wa[1] = va.y; wb[0] = vb.x; wb[1] = vb.y;
-          sa = scales2(blk[S::kKs + ka * S::kScales + t]);
-          sb = scales2(blk[S::kKs + kb * S::kScales + t]);
+            for (int i = 0; i < 4; ++i) sc[half][nt][i] = 0.f;
+          if (D == 128) {
+            const uint4 va = *reinterpret_cast<const uint4*>(blk + ka * S::kCodes + t * 16);
+            const uint4 vb = *reinterpret_cast<const uint4*>(blk + kb * S::kCodes + t * 16);
+            wa[half][0] = va.x; wa[half][1] = va.y; wa[half][KS / 2 - 2] = va.z; wa[half][KS / 2 - 1] = va.w;
+            wb[half][0] = vb.x; wb[half][1] = vb.y; wb[half][KS / 2 - 2] = vb.z; wb[half][KS / 2 - 1] = vb.w;
+            sa[half] = scales2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + ka * S::kScales + 2 * t));
+            sb[half] = scales2(*reinterpret_cast<const uint16_t*>(blk + S::kKs + kb * S::kScales + 2 * t));
+          } else {
+            const uint2 va = *reinterpret_cast<const uint2*>(blk + ka * S::kCodes + t * 8);
+            const uint2 vb = *reinterpret_cast<const uint2*>(blk + kb * S::kCodes + t * 8);
+            wa[half][0] = va.x; wa[half][1] = va.y; wb[half][0] = vb.x; wb[half][1] = vb.y;
+            sa[half] = scales2(blk[S::kKs + ka * S::kScales + t]);
+            sb[half] = scales2(blk[S::kKs + kb * S::kScales + t]);
+          }
         }
 #pragma unroll
         for (int w = 0; w < KS / 2; ++w) {
-          uint32_t ha[4], hb[4];
-          e2m1x8(wa[w], ha);
-          e2m1x8(wb[w], hb);
-          // 16 dims, two words, share a scale
-          const __half2 pa = w < 2 ? __low2half2(sa) : __high2half2(sa);
-          const __half2 pb = w < 2 ? __low2half2(sb) : __high2half2(sb);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { ha[i] = scaled(ha[i], pa); hb[i] = scaled(hb[i], pb); }
+          uint4 qw[QP][NT];
 #pragma unroll
           for (int p = 0; p < QP; ++p)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816(sc[half][nt], ha[0], hb[0], ha[1], hb[1], qf[p][nt][4 * w], qf[p][nt][4 * w + 1]);
-              mma16816(s2[nt], ha[2], hb[2], ha[3], hb[3], qf[p][nt][4 * w + 2], qf[p][nt][4 * w + 3]);
+              const uint32_t* f = qf[p][kQShared ? 0 : nt];
+              qw[p][nt] = kQShared ? q_shared[((p * NT + nt) * (KS / 2) + w) * 32]
+                                   : make_uint4(f[4 * w], f[4 * w + 1], f[4 * w + 2], f[4 * w + 3]);
             }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t ha[4], hb[4];
+            e2m1x8(wa[half][w], ha);
+            e2m1x8(wb[half][w], hb);
+            // 16 dims, two words, share a scale
+            const __half2 pa = w < 2 ? __low2half2(sa[half]) : __high2half2(sa[half]);
+            const __half2 pb = w < 2 ? __low2half2(sb[half]) : __high2half2(sb[half]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { ha[i] = scaled(ha[i], pa); hb[i] = scaled(hb[i], pb); }
+#pragma unroll
+            for (int p = 0; p < QP; ++p)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816(sc[half][nt], ha[0], hb[0], ha[1], hb[1], qw[p][nt].x, qw[p][nt].y);
+                mma16816(sc[half][nt], ha[2], hb[2], ha[3], hb[3], qw[p][nt].z, qw[p][nt].w);
+              }
+          }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[half][nt][i] += s2[nt][i];
       }
 
       if (masked) {
@@ -654,7 +685,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
 
     // ---- the piece is done: sums over the lanes that share a column
     const bool begins = b0 == 0;
-    float* to = ends ? part_at<D, R>(a.warp_part, blockIdx.x * kWarps + warp) : reinterpret_cast<float*>(ring);
+    float* to = reinterpret_cast<float*>(ring + (ends ? M::kFirst : 0));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -740,8 +771,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       for (int i = 0; i < kWarps; ++i) {
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < count) {
-          const float* p = code[i] & 1 ? reinterpret_cast<const float*>(ring_all + (size_t)(code[i] >> 1) * kStages * S::kBytes)
-                                       : part_at<D, R>(a.warp_part, blockIdx.x * kWarps + (code[i] >> 1));
+          const float* p = reinterpret_cast<const float*>(ring_all + (code[i] >> 1) * M::kWarp + (code[i] & 1 ? 0 : M::kFirst));
           v[i] = *reinterpret_cast<const float4*>(p + e);
         }
       }
@@ -782,7 +812,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
 // Blocks behind them, if asked: every key's weights go to its score.  All they
 // read of the first kernel's is found by one load, so that the rest is in
 // flight at once.
-constexpr int kThreadsM = 256;
+constexpr int kThreadsM = 512;
 constexpr int kWarpsM = kThreadsM / 32;
 
 // Running (maximum, sum) pairs of two partials.
@@ -793,8 +823,8 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
 }
 
 template <int D, int DT, int R>
-__global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const AttnArgs a) {
-  __shared__ float2 stat[kMaxRows];
+__global__ void __launch_bounds__(kThreadsM, 2) kv4_attn_merge_kernel(const AttnArgs a) {
+  __shared__ float2 stat[kMaxRows + 24];
   pdl_trigger();
   pdl_wait();
   const bool merges = (int)blockIdx.x < a.max_ctas;
@@ -820,9 +850,9 @@ __global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const Attn
     const int tile = item / a.c.heads, kvh = item - tile * a.c.heads;
     const int fours = min(R, a.rows - tile * R) * D / 4, share = c1 - c0;
     const int e0 = fours * (me - c0) / share, e1 = fours * (me - c0 + 1) / share;
-    // `wide` lanes to four elements, a partial each
+    // `wide` lanes to four elements, up to 4 partials each (their loads in flight together)
     int wide = 1;
-    while (wide < 32 && wide < c1 - c0 + 1) wide <<= 1;
+    while (wide < 32 && wide * 4 < c1 - c0 + 1) wide <<= 1;
     const int sub = lane & (wide - 1), at_once = kWarpsM * (32 / wide);
     for (int base = e0; base < e1; base += at_once) {   // the same number of rounds for every lane
       const int e = base + warp * (32 / wide) + lane / wide;
@@ -876,7 +906,7 @@ __global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const Attn
       const int k0 = b0 * kKv4Block + tid, k_end = min(n, b1 * kKv4Block);
       float* score = a.c.scores + ((size_t)seq * a.c.heads + kvh) * a.c.capacity();
       // up to 8 rows: the scores of this thread's first keys load beside the statistics
-      constexpr int kAhead = R == 8 ? 4 : 0;
+      constexpr int kAhead = R == 8 ? 2 : 0;
       float2 s[kAhead + 1][4];
       float old[kAhead + 1];
       const float* s_at = a.s_all + (size_t)(start + kvh * (nb + kStart) + kStart) * kKv4Block * a.s_rows;
@@ -953,23 +983,26 @@ __global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const Attn
 
 struct Layout {
   int R, tiles, s_rows;
-  size_t line, warp_part, cta_part, stats, s_all, bytes;   // byte offsets
+  size_t line, cta_part, stats, s_all, bytes;   // byte offsets
 };
 
-// Query rows of a KV head: one tile of 8 columns up to 8, else tiles of 16
-// (rows beyond share the widened cache of their tile; a tile of 32 would hold
-// 128 sums a thread and halve the warps).
-Layout layout_of(const mk_kv4_cache* c, int q_len, int group, bool accumulate) {
+// Query rows of a KV head: tiles of 8, 16 or 24, as many as share one widened
+// cache (32 would hold 128 sums a thread beside 64 scores and probabilities);
+// the shared memory of 24 fp32 rows of 128 dims is too much.
+int rows_of_tile(long long rows, int dtype, int d) {
+  return rows <= 8 ? 8 : rows <= 16 || (dtype == MK_DTYPE_F32 && d == 128) ? 16 : 24;
+}
+
+Layout layout_of(const mk_kv4_cache* c, int dtype, int q_len, int group, bool accumulate) {
   Layout l;
   const int rows = q_len * group, d = c->head_dim;
-  l.R = rows <= 8 ? 8 : 16;
+  l.R = rows_of_tile(rows, dtype, d);
   l.tiles = (rows + l.R - 1) / l.R;
   l.s_rows = l.tiles > 1 ? l.R : (rows + 1) & ~1;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t part = (size_t)l.R * (d + 2) * sizeof(float);
   size_t at = 0;
   l.line = at; at = up(at + (1 + 2 * kMaxCtas) * sizeof(int4));
-  l.warp_part = at; at = up(at + (size_t)kMaxCtas * kWarps * part);
   l.cta_part = at; at = up(at + (size_t)kMaxCtas * 2 * part);
   l.stats = l.s_all = at;
   if (accumulate) {
@@ -998,7 +1031,8 @@ int check_shape(const mk_kv4_cache* c, int q_len, int n_q_heads, const char* who
 
 template <int D, int DT, int NT>
 cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t st) {
-  constexpr int smem = kWarps * kStages * Kv4Shape<D>::kBytes;
+  constexpr int smem = AttnSmem<D, DT, NT>::kBytes;
+  static_assert(smem <= (NT == 1 ? 112 : 224) * 1024, "two CTAs an SM, or one");
   AttnArgs args = a;
   const int ctas = sms * (NT == 1 ? 2 : 1);
   args.max_ctas = ctas < kMaxCtas ? ctas : kMaxCtas;
@@ -1012,7 +1046,10 @@ cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t st) {
 
 template <int D, int DT>
 cudaError_t launch_rows(const AttnArgs& a, int R, int sms, cudaStream_t st) {
-  return R == 8 ? launch<D, DT, 1>(a, sms, st) : launch<D, DT, 2>(a, sms, st);
+  if (R == 8) return launch<D, DT, 1>(a, sms, st);
+  if constexpr (D == 64 || DT != MK_DTYPE_F32)
+    if (R == 24) return launch<D, DT, 3>(a, sms, st);
+  return launch<D, DT, 2>(a, sms, st);
 }
 
 template <int D>
@@ -1030,7 +1067,11 @@ using namespace mk;
 extern "C" size_t mk_attention_kv4_workspace_bytes(const mk_kv4_cache* cache, int q_len, int n_q_heads,
                                                    int accumulate) {
   if (check_shape(cache, q_len, n_q_heads, "mk_attention_kv4_workspace_bytes")) return 0;
-  return layout_of(cache, q_len, n_q_heads / cache->n_kv_heads, accumulate != 0).bytes;
+  // enough for every type
+  const int group = n_q_heads / cache->n_kv_heads;
+  const size_t a = layout_of(cache, MK_DTYPE_F32, q_len, group, accumulate != 0).bytes;
+  const size_t b = layout_of(cache, MK_DTYPE_BF16, q_len, group, accumulate != 0).bytes;
+  return a > b ? a : b;
 }
 
 extern "C" int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, int dtype, int q_len,
@@ -1051,7 +1092,7 @@ extern "C" int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, in
   if (accumulate && !cache->scores_dev)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "weights are added to a cache's scores, and this one has none");
   const int group = n_q_heads / cache->n_kv_heads;
-  const Layout l = layout_of(cache, q_len, group, accumulate != 0);
+  const Layout l = layout_of(cache, dtype, q_len, group, accumulate != 0);
   if (!workspace_dev || (reinterpret_cast<uintptr_t>(workspace_dev) & 15u) || workspace_bytes < l.bytes)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "the workspace is 16-byte aligned and of the bytes asked for");
   int dev = 0, sms = 0;
@@ -1069,7 +1110,6 @@ extern "C" int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, in
   a.o_mul = (float)exp2((double)cache->v_log2);
   a.max_ctas = 0;
   a.accumulate = accumulate != 0;
-  a.warp_part = reinterpret_cast<float*>(ws + l.warp_part);
   a.cta_part = reinterpret_cast<float*>(ws + l.cta_part);
   a.line = reinterpret_cast<int4*>(ws + l.line);
   a.edges = a.line + 1;
