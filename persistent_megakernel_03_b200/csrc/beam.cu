@@ -71,12 +71,14 @@ struct SelectArgs {
   int32_t* parents;
   float* scores;
   uint8_t* done;              // null: not wanted
-  int32_t dtype, beams, vocab, chunks, eos, wide;   // wide: 16-byte loads
+  int32_t beams, vocab, chunks, eos;
   // workspace
   float2* sums;               // [rows][chunks]: maximum, sum of exp(x - maximum)
   uint2* lists;               // [rows][chunks][beams]: key, token, highest first
 };
 
+// T: MK_DTYPE_* of the logits.  WIDE: rows allow 16-byte loads.
+template <int T, bool WIDE>
 __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs a) {
   __shared__ uint2 best[kWarpsS][kMaxBeams], list[kFound];
   __shared__ float tops[32], parts[kWarpsS];
@@ -89,58 +91,39 @@ __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs 
   const int c0 = blockIdx.x * kChunk;
   const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.stride;
   float x[kPer];
-  // wide: element e of load j is c0 + (j * threads + tid) * per + e, per = 4 or 8
-  const int per = a.wide ? (a.dtype == MK_DTYPE_F32 ? 4 : 8) : 1;
-  auto at = [&](int i) { return c0 + ((i / per) * kThreadsS + (int)threadIdx.x) * per + i % per; };
-  if (a.dtype == MK_DTYPE_F32) {
-    const float* p = reinterpret_cast<const float*>(base);
-    if (a.wide) {
+  // element e of load j is c0 + (j * threads + tid) * kLoad + e
+  constexpr int kSize = T == MK_DTYPE_F32 ? 4 : 2, kLoad = WIDE ? 16 / kSize : 1;
+  auto at = [&](int i) { return c0 + ((i / kLoad) * kThreadsS + (int)threadIdx.x) * kLoad + i % kLoad; };
+  auto widen = [&](uint32_t h) {
+    return T == MK_DTYPE_F32 ? __uint_as_float(h)
+           : T == MK_DTYPE_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+  };
+  auto one = [&](int i) {
+    if (i >= a.vocab) return -INFINITY;
+    return widen(kSize == 4 ? __ldcg(reinterpret_cast<const uint32_t*>(base) + i)
+                            : (uint32_t)__ldcg(reinterpret_cast<const uint16_t*>(base) + i));
+  };
+  if (WIDE && c0 + kChunk <= a.vocab) {
+    uint4 v[kPer / kLoad];
 #pragma unroll
-      for (int j = 0; j < kPer / 4; ++j) {
-        const int i = c0 + (j * kThreadsS + threadIdx.x) * 4;
-        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (i + 3 < a.vocab) v = __ldcg(reinterpret_cast<const float4*>(p + i));
-        else {
-          if (i < a.vocab) v.x = __ldcg(p + i);
-          if (i + 1 < a.vocab) v.y = __ldcg(p + i + 1);
-          if (i + 2 < a.vocab) v.z = __ldcg(p + i + 2);
-        }
-        x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
-      }
-    } else {
+    for (int j = 0; j < kPer / kLoad; ++j)
+      v[j] = __ldcg(reinterpret_cast<const uint4*>(base + (size_t)c0 * kSize) + j * kThreadsS + threadIdx.x);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = c0 + j * kThreadsS + threadIdx.x;
-        x[j] = i < a.vocab ? __ldcg(p + i) : -INFINITY;
-      }
-    }
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base);
-    const bool bf = a.dtype == MK_DTYPE_BF16;
-    auto widen = [&](uint32_t h) {
-      return bf ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
-    };
-    if (a.wide) {
+    for (int j = 0; j < kPer / kLoad; ++j) {
+      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int j = 0; j < kPer / 8; ++j) {
-        const int i = c0 + (j * kThreadsS + threadIdx.x) * 8;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        const bool whole = i + 7 < a.vocab;
-        if (whole) v = __ldcg(reinterpret_cast<const uint4*>(p + i));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (whole) x[8 * j + e] = widen(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
-          else x[8 * j + e] = i + e < a.vocab ? widen(__ldcg(p + i + e)) : -INFINITY;
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (kSize == 4) {
+          x[kLoad * j + e] = __uint_as_float(w[e]);
+        } else {
+          x[(kLoad * j + 2 * e) % kPer] = T == MK_DTYPE_BF16 ? __uint_as_float(w[e] << 16) : widen(w[e] & 0xFFFFu);
+          x[(kLoad * j + 2 * e + 1) % kPer] = T == MK_DTYPE_BF16 ? __uint_as_float(w[e] & 0xFFFF0000u) : widen(w[e] >> 16);
         }
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = c0 + j * kThreadsS + threadIdx.x;
-        x[j] = i < a.vocab ? widen(__ldcg(p + i)) : -INFINITY;
-      }
     }
+  } else {   // a row's last chunk, or rows at odd places
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = one(at(i));
   }
 
   // maxima of the threads (fmaxf passes NaN by), the groups, the chunk
@@ -517,14 +500,17 @@ extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_s
   a.logits = logits_dev; a.stride = (size_t)row_stride * esz;
   a.cum = cum_dev; a.finished = finished_dev;
   a.tokens = tokens_dev; a.parents = parents_dev; a.scores = scores_dev; a.done = finished_out_dev;
-  a.dtype = dtype; a.beams = beams; a.vocab = vocab; a.eos = eos;
+  a.beams = beams; a.vocab = vocab; a.eos = eos;
   a.chunks = (vocab + kChunk - 1) / kChunk;
-  a.wide = ((reinterpret_cast<uintptr_t>(logits_dev) | a.stride) & 15u) == 0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(logits_dev) | a.stride) & 15u) == 0;
   const size_t rows = (size_t)n_batch * beams;
   a.sums = static_cast<float2*>(workspace_dev);
   a.lists = reinterpret_cast<uint2*>(a.sums + rows * a.chunks);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pdl_launch(beam_chunk_kernel, dim3(a.chunks, (unsigned)rows), dim3(kThreadsS), 0, st, a);
+  auto chunk = dtype == MK_DTYPE_F32 ? (wide ? beam_chunk_kernel<MK_DTYPE_F32, true> : beam_chunk_kernel<MK_DTYPE_F32, false>)
+               : dtype == MK_DTYPE_BF16 ? (wide ? beam_chunk_kernel<MK_DTYPE_BF16, true> : beam_chunk_kernel<MK_DTYPE_BF16, false>)
+                                        : (wide ? beam_chunk_kernel<MK_DTYPE_F16, true> : beam_chunk_kernel<MK_DTYPE_F16, false>);
+  cudaError_t e = pdl_launch(chunk, dim3(a.chunks, (unsigned)rows), dim3(kThreadsS), 0, st, a);
   auto join = beams <= 4 ? (a.chunks <= 64 ? beam_join_kernel<2, 4> : beam_join_kernel<8, 4>)
               : beams <= 8 ? (a.chunks <= 64 ? beam_join_kernel<2, 8> : beam_join_kernel<8, 8>)
                            : (a.chunks <= 64 ? beam_join_kernel<2, 16> : beam_join_kernel<8, 16>);

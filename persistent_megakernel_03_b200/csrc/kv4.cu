@@ -53,30 +53,69 @@ Kv4 kv4_of(const mk_kv4_cache* c) {
 
 // ------------------------------------------------------------------ append
 
-// 16 input elements, raw, as fp32.
-__device__ __forceinline__ void widen_input(const uint4 (&raw)[4], int dtype, float (&x)[16]) {
-  if (dtype == MK_DTYPE_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[4 * i] = __uint_as_float(raw[i].x); x[4 * i + 1] = __uint_as_float(raw[i].y);
-      x[4 * i + 2] = __uint_as_float(raw[i].z); x[4 * i + 3] = __uint_as_float(raw[i].w);
-    }
-    return;
+// 32 bytes.  A thread's 16 elements are one or two such pieces: as one access
+// each they are whole sectors, while 16-byte accesses 32 bytes apart move every sector
+// twice.  Addresses that are only 16-byte aligned take those.
+__device__ __forceinline__ void load32(const uint8_t* p, bool whole, uint4& a, uint4& b) {
+  if (whole) {
+    asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+  } else {
+    a = __ldcg(reinterpret_cast<const uint4*>(p));
+    b = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
   }
+}
+__device__ __forceinline__ void store32(uint8_t* p, bool whole, uint4 a, uint4 b) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "l"(p)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = a;
+    reinterpret_cast<uint4*>(p)[1] = b;
+  }
+}
+
+// 16 input elements, raw, as fp32.
+template <int DT, int N>
+__device__ __forceinline__ void widen_input(const uint4 (&raw)[N], float (&x)[16]) {
+  constexpr int kPer = 16 / N;   // elements of 16 bytes
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < N; ++i) {
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (dtype == MK_DTYPE_BF16) {
-        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      if constexpr (DT == MK_DTYPE_F32) {
+        x[kPer * i + j] = __uint_as_float(w[j]);
+      } else if constexpr (DT == MK_DTYPE_BF16) {
+        x[kPer * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[kPer * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
       } else {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        x[8 * i + 2 * j] = f.x; x[8 * i + 2 * j + 1] = f.y;
+        x[kPer * i + 2 * j] = f.x; x[kPer * i + 2 * j + 1] = f.y;
       }
     }
   }
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // One group: the scale is e4m3(max |x| / 6), rounded to nearest even and at
@@ -113,14 +152,15 @@ __device__ __forceinline__ void quantize16(float (&x)[16], int neg_log2, uint2& 
   scale = two & 0x7Fu;
   const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2(scale) & 0xFFFFu)));
   const float inv = s > 0.f ? __frcp_rn(s) : 0.f;   // a scale of 0 makes every code 0
+  const uint64_t inv2 = pack2(inv, inv), minus_s2 = pack2(-s, -s);
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = x[8 * i + j], q = v * inv;
-      y[j] = fmaf(fmaf(-q, s, v), inv, q);
+    for (int j = 0; j < 8; j += 2) {   // two at a time (FFMA2)
+      const uint64_t u = pack2(x[8 * i + j], x[8 * i + j + 1]), q = mul2(u, inv2);
+      unpack2(fma2(fma2(q, minus_s2, u), inv2, q), y[j], y[j + 1]);
     }
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -144,31 +184,36 @@ constexpr int kAppendSmemSeq = 512;   // offsets kept in shared memory up to thi
 // tokens: where a token goes takes three dependent loads (offsets, length,
 // page), of which a CTA makes the first two once, and each thread's next
 // input is in flight while it rounds the current one.
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads, 3)
-    kv4_append_kernel(Kv4 c, const uint8_t* k, const uint8_t* v, int dtype, size_t k_stride, size_t v_stride,
-                      const int32_t* offsets, int n_tokens, int k_neg, int v_neg) {
+template <int D, int DT>
+__global__ void __launch_bounds__(kAppendThreads, DT == MK_DTYPE_F32 ? 3 : 4)
+    kv4_append_kernel(Kv4 c, const uint8_t* k, const uint8_t* v, size_t k_stride, size_t v_stride,
+                      bool whole, const int32_t* offsets, int n_tokens, int k_neg, int v_neg) {
   using S = Kv4Shape<D>;
   __shared__ int32_t offs[kAppendSmemSeq + 1], lens[kAppendSmemSeq];
   pdl_trigger();
   pdl_wait();
-  constexpr int G = D / kKv4Group;
-  const uint32_t per = c.heads * G, total = per * (uint32_t)n_tokens;   // threads of a token, of the call
-  const uint32_t step = gridDim.x * kAppendThreads;
-  uint32_t id = blockIdx.x * kAppendThreads + threadIdx.x;
-  const int esz = dtype == MK_DTYPE_F32 ? 4 : 2;
-  uint4 raw[2][4];
-  auto fetch = [&](uint32_t i) {
-    if (i >= total) return;
-    const uint32_t tok = i / per;
-    const size_t at = (size_t)(i - tok * per) * kKv4Group * esz;
-    const uint4* a = reinterpret_cast<const uint4*>(k + (size_t)tok * k_stride + at);
-    const uint4* b = reinterpret_cast<const uint4*>(v + (size_t)tok * v_stride + at);
+  constexpr int G = D / kKv4Group, esz = DT == MK_DTYPE_F32 ? 4 : 2;
+  // a thread keeps its part of a token (a head's group) and goes from token to
+  // token; a token of more parts than threads takes several CTAs
+  const int per = c.heads * G, at_once = max(kAppendThreads / per, 1), cuts = (per + kAppendThreads - 1) / kAppendThreads;
+  const int part = per <= kAppendThreads ? (int)threadIdx.x % per : (int)(blockIdx.x % cuts) * kAppendThreads + threadIdx.x;
+  int tok = per <= kAppendThreads ? (int)blockIdx.x * at_once + (int)threadIdx.x / per : (int)(blockIdx.x / cuts);
+  const int step = gridDim.x / cuts * at_once;
+  const bool mine = per <= kAppendThreads ? (int)threadIdx.x < at_once * per
+                                          : part < per && (int)blockIdx.x < (int)gridDim.x / cuts * cuts;
+  const int head = part / G, g = part % G;
+  k += (size_t)part * kKv4Group * esz;
+  v += (size_t)part * kKv4Group * esz;
+  uint4 raw[2][esz];
+  auto fetch = [&](int i) {
+    if (!mine || i >= n_tokens) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < 2 || esz == 4) { raw[0][j] = __ldcg(a + j); raw[1][j] = __ldcg(b + j); }
+    for (int j = 0; j < esz; j += 2) {
+      load32(k + (size_t)i * k_stride + 16 * j, whole, raw[0][j], raw[0][j + 1]);
+      load32(v + (size_t)i * v_stride + 16 * j, whole, raw[1][j], raw[1][j + 1]);
+    }
   };
-  fetch(id);
+  fetch(tok);
   const bool near = c.n_seq <= kAppendSmemSeq;
   if (near) {
     for (int i = threadIdx.x; i <= c.n_seq; i += kAppendThreads) {
@@ -177,11 +222,9 @@ __global__ void __launch_bounds__(kAppendThreads, 3)
     }
     __syncthreads();
   }
+  if (!mine) return;
   auto at = [&](int i) { return near ? offs[i] : __ldcg(offsets + i); };
-  for (; id < total; id += step) {
-    const int tok = (int)(id / per);
-    const uint32_t part = id - tok * per;
-    const int head = part / G, g = part % G;
+  for (; tok < n_tokens; tok += step) {
     int lo = 0, hi = c.n_seq - 1;   // the last sequence whose offset is <= tok
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -191,17 +234,17 @@ __global__ void __launch_bounds__(kAppendThreads, 3)
     const long long slot = (long long)(near ? lens[lo] : __ldcg(c.lens + lo)) - end + tok;
     // tokens before the first sequence or behind the last, slots out of range: nothing
     const bool ok = tok >= first && tok < end && slot >= 0 && slot < c.capacity();
-    const int lp = ok ? (int)slot / c.page_tokens : 0, in = (int)slot - lp * c.page_tokens;
+    const int lp = ok ? (int)((uint32_t)slot / (uint32_t)c.page_tokens) : 0, in = (int)slot - lp * c.page_tokens;
     const int page = ok ? c.page(lo, lp) : -1;
     uint2 codes[2];
     uint32_t scale[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[16];
-      widen_input(raw[i], dtype, x);
+      widen_input<DT>(raw[i], x);
       quantize16(x, i ? v_neg : k_neg, codes[i], scale[i]);
     }
-    fetch(id + step);
+    fetch(tok + step);
     if (page < 0) continue;
     uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
     const int row = in % kKv4Block;
@@ -216,24 +259,23 @@ __global__ void __launch_bounds__(kAppendThreads, 3)
 
 // -------------------------------------------------------------------- read
 
-__device__ __forceinline__ void store16(void* p, int dtype, const float (&x)[16]) {
+__device__ __forceinline__ void store16(uint8_t* p, int dtype, bool whole, const float (&x)[16]) {
+  uint32_t w[16];
   if (dtype == MK_DTYPE_F32) {
-    float4* f = static_cast<float4*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    return;
-  }
-  uint32_t w[8];
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (dtype == MK_DTYPE_BF16)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
-    else
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+    for (int j = 0; j < 8; ++j) {
+      if (dtype == MK_DTYPE_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+      else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+    }
   }
-  uint4* u = static_cast<uint4*>(p);
-  u[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  store32(p, whole, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+  if (dtype == MK_DTYPE_F32)
+    store32(p + 32, whole, make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
 }
 
 __device__ __forceinline__ void widen16(uint2 codes, uint32_t scale, float mul, float (&x)[16]) {
@@ -255,11 +297,13 @@ constexpr int kReadThreads = 256;
 
 // One thread per 16 dims of one slot's key and value.  Groups of a row, then
 // rows of a block, run along the threads: a warp reads 256 contiguous bytes
-// of codes and writes whole rows.
+// of codes and writes whole rows.  A slot's bytes are found by two dependent
+// loads (length and page, then the row), so many warps an SM matter more than
+// work per thread: four slots a thread took the same time for a ragged batch of
+// 7,300 slots and 5 to 10 us more for one of 4,096.
 template <int D>
 __global__ void __launch_bounds__(kReadThreads)
-    kv4_read_kernel(Kv4 c, int dtype, int n, uint8_t* k_out, uint8_t* v_out,
-                    float k_mul, float v_mul) {
+    kv4_read_kernel(Kv4 c, int dtype, int n, uint8_t* k_out, uint8_t* v_out, bool whole, float k_mul, float v_mul) {
   using S = Kv4Shape<D>;
   constexpr int G = D / kKv4Group, kRows = kReadThreads / G;
   pdl_trigger();
@@ -272,16 +316,16 @@ __global__ void __launch_bounds__(kReadThreads)
   if (slot >= n || slot >= len || page < 0) return;
   const uint8_t* b = kv4_block<D>(c, page, head, in / kKv4Block);
   const int row = in % kKv4Block;
-  const uint2 kc = *reinterpret_cast<const uint2*>(b + row * S::kCodes + g * 8);
-  const uint2 vc = *reinterpret_cast<const uint2*>(b + S::kVc + row * S::kCodes + g * 8);
-  const uint32_t ks = b[S::kKs + row * S::kScales + g], vs = b[S::kVs + row * S::kScales + g];
+  const uint2 kc = __ldcg(reinterpret_cast<const uint2*>(b + row * S::kCodes + g * 8));
+  const uint2 vc = __ldcg(reinterpret_cast<const uint2*>(b + S::kVc + row * S::kCodes + g * 8));
+  const uint32_t ks = __ldcg(b + S::kKs + row * S::kScales + g), vs = __ldcg(b + S::kVs + row * S::kScales + g);
   const size_t at = ((((size_t)s * n + slot) * c.heads + head) * D + g * kKv4Group) *
                     (dtype == MK_DTYPE_F32 ? 4 : 2);
   float x[16];
   widen16(kc, ks, k_mul, x);
-  store16(k_out + at, dtype, x);
+  store16(k_out + at, dtype, whole, x);
   widen16(vc, vs, v_mul, x);
-  store16(v_out + at, dtype, x);
+  store16(v_out + at, dtype, whole, x);
 }
 
 // ---------------------------------------------------------------- eviction
@@ -590,20 +634,25 @@ extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const
       (k_stride * esz) % 16 || (v_stride * esz) % 16)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "keys and values of a token are 16-byte aligned");
   const Kv4 c = kv4_of(cache);
-  const long long threads = (long long)n_tokens * c.heads * (cache->head_dim / kKv4Group);
-  long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
+  const int per = c.heads * (cache->head_dim / kKv4Group);   // threads of a token
+  const int at_once = per < kAppendThreads ? kAppendThreads / per : 1, cuts = (per + kAppendThreads - 1) / kAppendThreads;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return kv4_fail(MK_ERR_CUDA, who, "no device");
-  if (blocks > 3ll * sms) blocks = 3ll * sms;
-  if (threads > 0x7FFFFFFFll - 1024 * kAppendThreads) return kv4_fail(MK_ERR_INVALID_ARG, who, "too many tokens in one call");
+  const int wave = (dtype == MK_DTYPE_F32 ? 3 : 4) * sms;
+  long long blocks = ((long long)n_tokens + at_once - 1) / at_once * cuts;
+  if (blocks > wave) blocks = wave > cuts ? wave / cuts * cuts : cuts;
   const uint8_t* k = static_cast<const uint8_t*>(k_dev);
   const uint8_t* v = static_cast<const uint8_t*>(v_dev);
   const size_t ks = (size_t)k_stride * esz, vs = (size_t)v_stride * esz;
-  auto kernel = cache->head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>;
+  const bool whole = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | ks | vs) & 31u) == 0;
+  const bool wide = cache->head_dim == 128;
+  auto kernel = dtype == MK_DTYPE_F32 ? (wide ? kv4_append_kernel<128, MK_DTYPE_F32> : kv4_append_kernel<64, MK_DTYPE_F32>)
+                : dtype == MK_DTYPE_BF16 ? (wide ? kv4_append_kernel<128, MK_DTYPE_BF16> : kv4_append_kernel<64, MK_DTYPE_BF16>)
+                                         : (wide ? kv4_append_kernel<128, MK_DTYPE_F16> : kv4_append_kernel<64, MK_DTYPE_F16>);
   const cudaError_t e = pdl_launch(kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0,
-                                   static_cast<cudaStream_t>(stream), c, k, v, dtype, ks, vs, offsets_dev,
+                                   static_cast<cudaStream_t>(stream), c, k, v, ks, vs, whole, offsets_dev,
                                    n_tokens, -cache->k_log2, -cache->v_log2);
   return e == cudaSuccess ? MK_OK : kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
 }
@@ -621,10 +670,11 @@ extern "C" int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_
   const Kv4 c = kv4_of(cache);
   const int rows = kReadThreads / (cache->head_dim / kKv4Group);
   const int most = n < c.capacity() ? n : c.capacity();
+  const bool whole = ((reinterpret_cast<uintptr_t>(k_out_dev) | reinterpret_cast<uintptr_t>(v_out_dev)) & 31u) == 0;
   auto kernel = cache->head_dim == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
   const cudaError_t e = pdl_launch(kernel, dim3((unsigned)((most + rows - 1) / rows), c.heads, c.n_seq),
                                    dim3(kReadThreads), 0, static_cast<cudaStream_t>(stream), c, dtype, n,
-                                   static_cast<uint8_t*>(k_out_dev), static_cast<uint8_t*>(v_out_dev),
+                                   static_cast<uint8_t*>(k_out_dev), static_cast<uint8_t*>(v_out_dev), whole,
                                    ldexpf(1.f, cache->k_log2), ldexpf(1.f, cache->v_log2));
   return e == cudaSuccess ? MK_OK : kv4_fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
 }

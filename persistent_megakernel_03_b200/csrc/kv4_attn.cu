@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   // pieces that a warp leaves: even its first, in a place of its own, odd its last, in its ring's
   __shared__ int4 piece_of[2 * kWarps];    // sequence, item (-1: none), first block's unit, blocks
   __shared__ float piece_max[2 * kWarps][R], piece_sum[2 * kWarps][R];
-  __shared__ float weight[kWarps][R], total[R];
+  __shared__ float total[R];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
@@ -729,58 +729,50 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
   // ---- pieces of the CTA's warps that belong together, in order: the last of
   // a warp, those of warps that lie whole in the item, the first of the one
   // where it ends
-  // pieces [first, first + count) of those in `mask`; the final one ends the item, or not
-  auto merge = [&](uint32_t mask, int count, bool ends) {
-    int code[kWarps];
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      code[i] = i < count ? __ffs(mask) - 1 : 0;
-      mask &= mask - 1u;
-    }
-    const int4 who = piece_of[code[0]];
+  // pieces in `mask`, in order: `count` of warps that follow one another; the final
+  // one ends the item, or not
+  auto merge = [&](uint32_t mask, bool ends) {
+    const int c0 = __ffs(mask) - 1, count = __popc(mask);
+    const int4 who = piece_of[c0];
     const bool done = who.w < 0 && ends;   // begins and ends in this CTA
     const int tile = who.y / a.c.heads, kvh = who.y - tile * a.c.heads;
     const int rows = min(R, a.rows - tile * R);
     float* slot = part_at<D, R>(a.cta_part, blockIdx.x * 2 + (ends ? 0 : 1));
-    if ((int)threadIdx.x < R) {
-      const int row = threadIdx.x;
-      float m = -INFINITY, l = 0.f;
+    // weights: 16 lanes to a row, a possible piece each
+    for (int row = threadIdx.x >> 4; row < (R + 15) / 16 * 16; row += kThreadsA / 16) {
+      const int code = threadIdx.x & 15;
+      const bool in = row < R && (mask >> code & 1u);
+      const float mi = in ? piece_max[code][row] : -INFINITY;
+      float m = mi;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i)
-        if (i < count) m = fmaxf(m, piece_max[code[i]][row]);
+      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const float f = in ? rescale(mi, m) : 0.f;
+      float l = in ? f * piece_sum[code][row] : 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float f = i < count ? rescale(piece_max[code[i]][row], m) : 0.f;
-        weight[i][row] = f;
-        if (i < count) l = fmaf(f, piece_sum[code[i]][row], l);
-      }
-      total[row] = l;
-      if (!done) {
-        slot[R * D + row] = m;
-        slot[R * D + R + row] = l;
-      } else if (a.accumulate) {
-        a.stats[((size_t)who.x * items + who.y) * R + row] = make_float2(m, l);
+      for (int o = 8; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+      if (in) piece_max[code][row] = f;   // from here on its weight
+      if (code == 0 && row < R) {
+        total[row] = l;
+        if (!done) {
+          slot[R * D + row] = m;
+          slot[R * D + R + row] = l;
+        } else if (a.accumulate) {
+          a.stats[((size_t)who.x * items + who.y) * R + row] = make_float2(m, l);
+        }
       }
     }
     if (!ends && threadIdx.x == 0) a.edges[blockIdx.x] = make_int4(who.x, who.y, who.z, abs(who.w));
     __syncthreads();
     for (int e = threadIdx.x * 4; e < rows * D; e += kThreadsA * 4) {
       const int row = e / D;
-      float4 v[kWarps];
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < count) {
-          const float* p = reinterpret_cast<const float*>(ring_all + (code[i] >> 1) * M::kWarp + (code[i] & 1 ? 0 : M::kFirst));
-          v[i] = *reinterpret_cast<const float4*>(p + e);
-        }
-      }
       float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float f = weight[i][row];   // 0 behind the last
-        x[0] = fmaf(f, v[i].x, x[0]); x[1] = fmaf(f, v[i].y, x[1]);
-        x[2] = fmaf(f, v[i].z, x[2]); x[3] = fmaf(f, v[i].w, x[3]);
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
+        const int code = i == 0 ? c0 : (c0 & ~1) + 2 * i + (ends && i == count - 1 ? 0 : 1);
+        const float4 v = *reinterpret_cast<const float4*>(ring_all + (code >> 1) * M::kWarp + (code & 1 ? 0 : M::kFirst) + e * 4);
+        const float f = piece_max[code][row];
+        x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]);
+        x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
       }
       if (done) {
         size_t at;
@@ -793,14 +785,15 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
         *reinterpret_cast<float4*>(slot + e) = make_float4(x[0], x[1], x[2], x[3]);
       }
     }
-    __syncthreads();   // the weights are free
+    __syncthreads();   // the sums are free
   };
   uint32_t pieces = __ballot_sync(0xFFFFFFFFu, lane < 2 * kWarps && piece_of[lane & (2 * kWarps - 1)].y >= 0);
   bool open = false;
+#pragma unroll 1
   while (pieces) {   // up to the next first piece (an even one), which ends its item
     const uint32_t even = pieces & 0x55555555u;
     const uint32_t now = even ? pieces & (even ^ (even - 1u)) : pieces;
-    merge(now, __popc(now), even != 0u);
+    merge(now, even != 0u);
     pieces &= ~now;
     open = even == 0u;
   }
@@ -812,7 +805,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
 // Blocks behind them, if asked: every key's weights go to its score.  All they
 // read of the first kernel's is found by one load, so that the rest is in
 // flight at once.
-constexpr int kThreadsM = 512;
+constexpr int kThreadsM = 256;
 constexpr int kWarpsM = kThreadsM / 32;
 
 // Running (maximum, sum) pairs of two partials.
@@ -823,7 +816,7 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
 }
 
 template <int D, int DT, int R>
-__global__ void __launch_bounds__(kThreadsM, 2) kv4_attn_merge_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const AttnArgs a) {
   __shared__ float2 stat[kMaxRows + 24];
   pdl_trigger();
   pdl_wait();
@@ -906,7 +899,7 @@ __global__ void __launch_bounds__(kThreadsM, 2) kv4_attn_merge_kernel(const Attn
       const int k0 = b0 * kKv4Block + tid, k_end = min(n, b1 * kKv4Block);
       float* score = a.c.scores + ((size_t)seq * a.c.heads + kvh) * a.c.capacity();
       // up to 8 rows: the scores of this thread's first keys load beside the statistics
-      constexpr int kAhead = R == 8 ? 2 : 0;
+      constexpr int kAhead = R == 8 ? 4 : 0;
       float2 s[kAhead + 1][4];
       float old[kAhead + 1];
       const float* s_at = a.s_all + (size_t)(start + kvh * (nb + kStart) + kStart) * kKv4Block * a.s_rows;
