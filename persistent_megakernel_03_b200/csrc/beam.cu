@@ -15,7 +15,7 @@ namespace {
 // Candidate (b, v) of a search has the score cum[b] + logit[b][v] - lse(logit[b]);
 // the W highest are wanted.  Inside a beam the order is that of the logits, so
 // no score is needed to find a beam's own W best: the vocabulary is read once,
-// in chunks of 4,096 that stay in registers, and each chunk gives its W
+// in chunks of 16 KB that stay in registers, and each chunk gives its W
 // highest logits, its maximum and its sum of exponentials.  The W-th highest
 // maximum of the chunk's 32 groups of 8 threads bounds the W-th highest logit
 // from below, so only logits from that bound on are looked at again, a few
@@ -32,12 +32,15 @@ namespace {
 
 constexpr int kThreadsS = 256;
 constexpr int kWarpsS = kThreadsS / 32;
-constexpr int kPer = 16;                        // logits of a thread
-constexpr int kChunk = kThreadsS * kPer;
+// A chunk is 16 KB of logits: 64 bytes a thread.
+__host__ __device__ constexpr int per_thread(int dtype) { return dtype == MK_DTYPE_F32 ? 16 : 32; }
+__host__ __device__ constexpr int chunk_of(int dtype) { return kThreadsS * per_thread(dtype); }
 constexpr int kMaxBeams = 16;
 constexpr int kFound = 128;                     // logits from the bound on that a chunk keeps
 static_assert(kWarpsS * 4 == 32, "a group's maximum for every lane");
-constexpr int kMaxChunks = 256;                 // vocabulary up to 1,048,576
+constexpr int kMaxChunks = 256;
+constexpr int kMaxVocab = 1 << 20;
+static_assert(kMaxVocab <= chunk_of(MK_DTYPE_F32) * kMaxChunks, "chunk heads that a join holds");
 
 // fp32 to an integer of the same order; 0 for what is no candidate (-inf, NaN).
 __device__ __forceinline__ uint32_t logit_key(float f) {
@@ -80,8 +83,10 @@ struct SelectArgs {
 // T: MK_DTYPE_* of the logits.  WIDE: rows allow 16-byte loads.
 template <int T, bool WIDE>
 __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs a) {
+  constexpr int kPer = per_thread(T), kChunk = chunk_of(T);
   __shared__ uint2 best[kWarpsS][kMaxBeams], list[kFound];
   __shared__ float tops[32], parts[kWarpsS];
+  __shared__ uint2 borders;   // keys of the highest logit and of the bound
   __shared__ int found;
   pdl_trigger();
   pdl_wait();
@@ -136,28 +141,38 @@ __global__ void __launch_bounds__(kThreadsS) beam_chunk_kernel(const SelectArgs 
   if ((lane & 7) == 0) tops[warp * 4 + (lane >> 3)] = group;
   if (threadIdx.x == 0) found = 0;
   __syncthreads();
-  uint32_t left = logit_key(tops[lane]);   // a group a lane
-  const uint32_t highest = __reduce_max_sync(0xFFFFFFFFu, left);
-  const float mx = highest ? key_logit(highest) : 0.f;
-  uint32_t bound = highest;
-  for (int j = 0; j < W; ++j) {
-    bound = __reduce_max_sync(0xFFFFFFFFu, left);
-    if (bound == 0u) break;   // fewer groups with a candidate: look at every one
-    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0u;
+  if (warp == 0) {
+    uint32_t left = logit_key(tops[lane]);   // a group a lane
+    const uint32_t first = __reduce_max_sync(0xFFFFFFFFu, left);
+    uint32_t last = first;
+    for (int j = 0; j < W; ++j) {
+      last = __reduce_max_sync(0xFFFFFFFFu, left);
+      if (last == 0u) break;   // fewer groups with a candidate: look at every one
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == last)) - 1) left = 0u;
+    }
+    if (lane == 0) borders = make_uint2(first, last);
   }
+  __syncthreads();
+  const uint32_t highest = borders.x, bound = borders.y;
+  const float mx = highest ? key_logit(highest) : 0.f;
   // the W-th highest maximum, or everything
   const float least = bound ? key_logit(bound) : -INFINITY;
-  if (top >= least && top > -INFINITY) {
+  if (__any_sync(0xFFFFFFFFu, top >= least && top > -INFINITY)) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (x[i] >= least && x[i] > -INFINITY) {
-        const int to = atomicAdd(&found, 1);   // any order: places decide below
-        if (to < kFound) list[to] = make_uint2(logit_key(x[i]), at(i));
+    for (int i = 0; i < kPer; ++i) {
+      const bool hit = x[i] >= least && x[i] > -INFINITY;
+      if (__any_sync(0xFFFFFFFFu, hit)) {   // few of a warp's elements: the rest costs a vote
+        if (hit) {
+          const int to = atomicAdd(&found, 1);   // any order: places decide below
+          if (to < kFound) list[to] = make_uint2(logit_key(x[i]), at(i));
+        }
       }
+    }
   }
-  float sum = 0.f;
+  float part[4] = {0.f, 0.f, 0.f, 0.f};   // -inf adds 0, NaN goes through
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sum += ex2((x[i] - mx) * 1.44269504f);   // -inf adds 0, NaN goes through
+  for (int i = 0; i < kPer; ++i) part[i & 3] += ex2((x[i] - mx) * 1.44269504f);
+  float sum = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane == 0) parts[warp] = sum;
@@ -238,17 +253,19 @@ __device__ __forceinline__ unsigned long long score_key64(double s) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-// One CTA a search, one warp a beam.  Every choice of the first W of a few is
-// made by rank: each candidate counts those before it, without a chain of
-// rounds.  HEADS: chunk heads of a lane.  WT: most beams.
+__device__ __forceinline__ bool finished_of(const SelectArgs& a, size_t row) {
+  return a.finished && __ldcg(a.finished + row);
+}
+
+// One CTA a search, one warp a beam.  HEADS: chunk heads of a lane.  WT: most beams.
 template <int HEADS, int WT>
 __global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) {
   constexpr int kOwn = WT * WT < 32 ? 1 : WT * WT / 32;   // candidates of a lane
-  __shared__ uint2 few[WT][HEADS * 32 > WT * WT ? HEADS * 32 : WT * WT];   // a beam's heads, then its lists
+  __shared__ __align__(16) uint2 few[WT][HEADS * 32 > WT * WT ? HEADS * 32 : WT * WT];   // heads, then candidates
   __shared__ int chosen[WT][WT];
-  __shared__ unsigned long long cand_key[WT * WT];
-  __shared__ double cand_score[WT * WT];
-  __shared__ int32_t cand_token[WT * WT];
+  __shared__ uint32_t bound[WT];
+  __shared__ double cand_score[WT][WT];
+  __shared__ int32_t cand_token[WT][WT];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5, W = a.beams;
@@ -257,7 +274,7 @@ __global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) 
   const uint2* lists = a.lists + row * a.chunks * W;
   // all in flight at once (a finished beam's are not written: not used)
   const double cum = __ldcg(a.cum + row);
-  const bool finished = a.finished && __ldcg(a.finished + row);
+  const bool finished = finished_of(a, row);
   float2 sum_of[HEADS];
   uint2 head[HEADS];
 #pragma unroll
@@ -267,30 +284,41 @@ __global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) 
     head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
   }
   for (int j = lane; j < W; j += 32) {   // no candidates so far
-    cand_key[beam * W + j] = 0ull;
+    cand_score[beam][j] = -INFINITY;
     chosen[beam][j] = -1;
   }
+  if (lane == 0) bound[beam] = 0u;
   if (finished) {
+    __syncwarp();
     if (lane == 0) {
-      cand_key[beam * W] = score_key64(cum);
-      cand_score[beam * W] = cum;
-      cand_token[beam * W] = a.eos;
+      cand_score[beam][0] = cum;
+      cand_token[beam][0] = a.eos;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < HEADS; ++i) few[beam][i * 32 + lane] = head[i];
     __syncwarp();
-    // the W chunks with the highest heads (a head's token tells ties apart)
-    const int live = min(a.chunks, HEADS * 32);
+    // the W chunks with the highest heads, by counting the heads before each (a
+    // head's token tells ties apart); the last of them bounds the beam's W best
+    const uint4* two = reinterpret_cast<const uint4*>(few[beam]);
+    int rank[HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) rank[i] = 0;
+    const int pairs = (min(a.chunks, HEADS * 32) + 1) / 2;
+#pragma unroll 4
+    for (int j = 0; j < pairs; ++j) {
+      const uint4 o = two[j];
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        rank[i] += o.x > head[i].x || (o.x == head[i].x && o.y < head[i].y);
+        rank[i] += o.z > head[i].x || (o.z == head[i].x && o.w < head[i].y);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < HEADS; ++i)
-      if (head[i].x) {
-        int rank = 0;
-        for (int j = 0; j < live; ++j) {
-          const uint2 o = few[beam][j];
-          rank += o.x > head[i].x || (o.x == head[i].x && o.y < head[i].y);
-        }
-        if (rank < W) chosen[beam][rank] = i * 32 + lane;
+      if (head[i].x && rank[i] < W) {
+        chosen[beam][rank[i]] = i * 32 + lane;
+        if (rank[i] == W - 1) bound[beam] = head[i].x;
       }
     __syncwarp();
     // their lists, in flight during the log-sum-exp over all chunks
@@ -314,61 +342,54 @@ __global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) 
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     const double lse = (double)mx + log(sum);
-    // the beam's W best of W * W
-    __syncwarp();
+    // the beam's W best: of the few from the bound on, again by counting
+    const uint32_t least = max(bound[beam], 1u);
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (i * 32 + lane < W * W) few[beam][i * 32 + lane] = c[i];
+    for (int i = 0; i < kOwn; ++i) {
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, c[i].x >= least);
+      if (c[i].x >= least) few[beam][n + __popc(in & ((1u << lane) - 1u))] = c[i];
+      n += __popc(in);
+    }
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (c[i].x) {
-        int rank = 0;
-        for (int j = 0; j < W * W; ++j) {
-          const uint2 o = few[beam][j];
-          rank += o.x > c[i].x || (o.x == c[i].x && o.y < c[i].y);
-        }
-        if (rank < W) {
-          const double s = cum + ((double)key_logit(c[i].x) - lse);
-          cand_key[beam * W + rank] = score_key64(s);
-          cand_score[beam * W + rank] = s;
-          cand_token[beam * W + rank] = (int32_t)c[i].y;
-        }
+    for (int e = lane; e < n; e += 32) {
+      const uint2 me = few[beam][e];
+      int before = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const uint2 o = few[beam][j];
+        before += o.x > me.x || (o.x == me.x && o.y < me.y);
       }
+      if (before < W) {
+        cand_score[beam][before] = cum + ((double)key_logit(me.x) - lse);
+        cand_token[beam][before] = (int32_t)me.y;
+      }
+    }
   }
   __syncthreads();
-  // the W first of W * W: highest score, then lowest beam, then the beam's own
-  // order; a dead beam, which keeps its own state, behind the last candidate
-  int live = 0;
-  for (int e = threadIdx.x; e < W * W; e += 32 * W) {
-    const unsigned long long k = cand_key[e];
-    int rank = 0;
-    live = 0;
-    for (int j = 0; j < W * W; ++j) {
-      const unsigned long long o = cand_key[j];
-      rank += o > k || (o == k && j < e);
-      live += o != 0ull;
-    }
-    const bool real = k != 0ull;
-    if (real && rank < W) {
-      const size_t to = (size_t)blockIdx.x * W + rank;
-      const int parent = e / W, token = cand_token[e];
+  if (beam) return;
+  // W rounds over the beams' lists, a lane each: highest score, then lowest beam
+  int at = 0;
+  double mine = lane < W ? cand_score[lane][0] : -INFINITY;
+  for (int j = 0; j < W; ++j) {
+    const unsigned long long key = score_key64(mine);
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32));
+    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
+    const bool real = (hi | lo) != 0u;
+    const int who = __ffs(__ballot_sync(0xFFFFFFFFu, key == ((unsigned long long)hi << 32 | lo))) - 1;
+    // fewer candidates than beams: a dead one, which keeps its own state
+    if (real ? lane == who : lane == j) {
+      const size_t to = (size_t)blockIdx.x * W + j;
+      const int token = real ? cand_token[lane][at] : max(a.eos, 0);
       a.tokens[to] = token;
-      a.parents[to] = parent;
-      a.scores[to] = (float)cand_score[e];
-      if (a.done)
-        a.done[to] = (a.finished && __ldcg(a.finished + (size_t)blockIdx.x * W + parent)) ||
-                     (a.eos >= 0 && token == a.eos);
+      a.parents[to] = lane;
+      a.scores[to] = real ? (float)mine : -INFINITY;
+      if (a.done) a.done[to] = finished_of(a, (size_t)blockIdx.x * W + lane) || (a.eos >= 0 && token == a.eos);
+      if (real) {
+        ++at;
+        mine = at < W ? cand_score[lane][at] : -INFINITY;
+      }
     }
-  }
-  // threads 0 .. W - 1 have counted the live ones (W <= W * W)
-  if ((int)threadIdx.x < W && (int)threadIdx.x >= live) {
-    const int j = threadIdx.x;
-    const size_t to = (size_t)blockIdx.x * W + j;
-    a.tokens[to] = max(a.eos, 0);
-    a.parents[to] = j;
-    a.scores[to] = -INFINITY;
-    if (a.done) a.done[to] = (a.finished && __ldcg(a.finished + to)) || a.eos >= 0;
   }
 }
 
@@ -462,10 +483,11 @@ cudaError_t launch_reorder(const ReorderArgs& a, int n_batch, cudaStream_t st) {
 using namespace mk;
 
 extern "C" size_t mk_beam_select_workspace_bytes(int n_batch, int beams, int vocab) {
-  if (n_batch < 1 || beams < 1 || beams > kMaxBeams || vocab < 1 || vocab > kChunk * kMaxChunks ||
+  if (n_batch < 1 || beams < 1 || beams > kMaxBeams || vocab < 1 || vocab > kMaxVocab ||
       (long long)n_batch * beams > 65535)
     return 0;
-  const size_t chunks = (vocab + kChunk - 1) / kChunk, rows = (size_t)n_batch * beams;
+  const int per = chunk_of(MK_DTYPE_F32);   // enough for every type
+  const size_t chunks = (vocab + per - 1) / per, rows = (size_t)n_batch * beams;
   return rows * chunks * (sizeof(float2) + beams * sizeof(uint2));
 }
 
@@ -477,7 +499,7 @@ extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_s
   const char* who = "mk_beam_select";
   if (n_batch < 1 || beams < 1 || beams > kMaxBeams || (long long)n_batch * beams > 65535)
     return fail(MK_ERR_INVALID_ARG, who, "1 to 16 beams, and at most 65535 rows");
-  if (vocab < 1 || vocab > kChunk * kMaxChunks) return fail(MK_ERR_INVALID_ARG, who, "vocab is 1 to 1048576");
+  if (vocab < 1 || vocab > kMaxVocab) return fail(MK_ERR_INVALID_ARG, who, "vocab is 1 to 1048576");
   const int esz = dtype == MK_DTYPE_F32 ? 4 : (dtype == MK_DTYPE_BF16 || dtype == MK_DTYPE_F16) ? 2 : 0;
   if (!esz) return fail(MK_ERR_INVALID_ARG, who, "dtype is one of MK_DTYPE_*");
   if (!logits_dev || !cum_dev || !tokens_dev || !parents_dev || !scores_dev)
@@ -501,7 +523,7 @@ extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_s
   a.cum = cum_dev; a.finished = finished_dev;
   a.tokens = tokens_dev; a.parents = parents_dev; a.scores = scores_dev; a.done = finished_out_dev;
   a.beams = beams; a.vocab = vocab; a.eos = eos;
-  a.chunks = (vocab + kChunk - 1) / kChunk;
+  a.chunks = (vocab + chunk_of(dtype) - 1) / chunk_of(dtype);
   const bool wide = ((reinterpret_cast<uintptr_t>(logits_dev) | a.stride) & 15u) == 0;
   const size_t rows = (size_t)n_batch * beams;
   a.sums = static_cast<float2*>(workspace_dev);
