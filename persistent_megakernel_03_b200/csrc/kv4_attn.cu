@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       }
 
       // O^T, 16 keys at a time
+      bool some_nan = false;   // among the values that only some rows see
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         constexpr int W = D / 64;   // words of a key's dims that lane r holds: 16 dims or 8
@@ -637,7 +638,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = b * kKv4Block + half * 16 + t + 4 * i;
-            if (!there || at >= this_n || (at >= see_all && (s[i] & 0x7Fu) == 0x7Fu)) s[i] = 0u;
+            const bool apart = there && at >= see_all && at < this_n && (s[i] & 0x7Fu) == 0x7Fu;
+            if (!there || at >= this_n || apart) s[i] = 0u;
+            some_nan |= apart;
           }
         }
         const __half2 s01 = scales2(s[0] | s[1] << 8), s23 = scales2(s[2] | s[3] << 8);
@@ -662,11 +665,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
           }
         }
       }
-      if (masked && there && see_all < this_n) {
-        // NaN values among keys that only some rows see
-        for (int key = 0; key < kKv4Block; ++key) {
-          const int at = b * kKv4Block + key;
-          if (at < see_all || at >= this_n) continue;
+      if (masked && __any_sync(0xFFFFFFFFu, some_nan)) {
+        for (int at = max(see_all, b * kKv4Block); at < min(this_n, (b + 1) * kKv4Block); ++at) {
+          const int key = at - b * kKv4Block;
           if ((blk[S::kVs + key * S::kScales + (D == 128 ? r : r >> 1)] & 0x7Fu) != 0x7Fu) continue;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
