@@ -423,7 +423,7 @@ size_t mk_kv4_page_bytes(int n_kv_heads, int head_dim, int page_tokens);
  * a code is the e2m1 value nearest to x / scale, halves to the even code, both
  * decided exactly; |x| past 2688 * 2^log2 saturates, and a group that holds a
  * NaN or an infinity reads back as NaN.  offsets_dev: n_seq + 1 int32, not
- * decreasing; tokens outside them, slots outside the capacity and slots without a
+ * decreasing; n_tokens <= 2^30.  Tokens outside them, slots outside the capacity and slots without a
  * page are skipped.  Sequences must not share a page that is written. */
 int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const void* v_dev, int dtype,
                   long long k_stride, long long v_stride, const int32_t* offsets_dev, int n_tokens,
@@ -440,8 +440,9 @@ int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, vo
  * query heads: token i of sequence s sees slots j < lens[s] - q_len + i + 1
  * (its own key included), out = softmax(scale * q k^T) v.  q_dev: `dtype`
  * [n_seq * q_len][n_q_heads][head_dim], tokens q_stride elements apart, 16-byte
- * aligned; query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
- * n_q_heads / n_kv_heads <= 1024.  out_dev: the same type,
+ * aligned, finite (a row that is not gets NaN or infinities, the others stay
+ * right); query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
+ * n_q_heads / n_kv_heads <= 1024; 1e-18 <= scale <= 1e18.  out_dev: the same type,
  * [n_seq][q_len][n_q_heads][head_dim], 16-byte aligned.  fp32 softmax and sums; queries and
  * probabilities enter the products with at least 22 bits (probabilities of a
  * bf16 call 11).  A token that sees nothing gets zeros (a sequence shorter than
@@ -449,7 +450,8 @@ int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, vo
  * slot holds never matters.  accumulate != 0 adds, for every slot, the weights
  * of all tokens and query heads of its KV head to the cache's scores.
  * workspace_dev: mk_attention_kv4_workspace_bytes(...) bytes (0: an argument
- * is not supported), 16-byte aligned, any contents. */
+ * is not supported), 16-byte aligned, any contents; with accumulate it grows
+ * with n_seq * capacity * rows (the scores of every slot). */
 size_t mk_attention_kv4_workspace_bytes(const mk_kv4_cache* cache, int q_len, int n_q_heads,
                                         int accumulate);
 int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, int dtype, int q_len,

@@ -608,14 +608,18 @@ class Kv4Cache:
 
 
 def _rows(t, heads, dim, what, device):
-    """(pointer, elements between tokens) of token rows [tokens, heads, dim]
-    whose heads lie together."""
-    if t.get_device() != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: [tokens, {heads}, {dim}] on the cache's device expected, got {tuple(t.shape)}")
+    """(pointer, elements between tokens, tokens) of token rows [tokens, heads,
+    dim] whose heads lie together."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.get_device() != device:
+        raise ValueError(f"{what}: [tokens, {heads}, {dim}] on the cache's device expected, got {tuple(shape)}")
+    n = shape[0]
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim, n
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{what}: a token's heads and dims are contiguous")
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), st[0] if n > 1 else heads * dim, n
 
 
 def kv4_append(cache: Kv4Cache, k, v, offsets, stream=None):
@@ -623,12 +627,12 @@ def kv4_append(cache: Kv4Cache, k, v, offsets, stream=None):
     strided) into the cache; tokens offsets[s]..offsets[s+1] are the newest of
     sequence s, which cache.lens counts already (see mk_kv4_append)."""
     d = cache.device
-    kp, ks = _rows(k, cache.n_kv_heads, cache.head_dim, "k", d)
-    vp, vs = _rows(v, cache.n_kv_heads, cache.head_dim, "v", d)
-    n = k.shape[0]
-    if n != v.shape[0] or k.dtype != v.dtype:
+    kp, ks, n = _rows(k, cache.n_kv_heads, cache.head_dim, "k", d)
+    vp, vs, m = _rows(v, cache.n_kv_heads, cache.head_dim, "v", d)
+    code = _dtype(k)
+    if n != m or _dtype(v) != code:
         raise ValueError("k and v have the same tokens and type")
-    _on(d, stream, lib().mk_kv4_append, cache.ref, kp, vp, _dtype(k), ks, vs,
+    _on(d, stream, lib().mk_kv4_append, cache.ref, kp, vp, code, ks, vs,
         _tensor(offsets, torch.int32, "offsets", (cache.n_seq + 1,), d), n)
 
 

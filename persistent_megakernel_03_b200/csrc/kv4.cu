@@ -2,6 +2,7 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -14,6 +15,17 @@ int kv4_fail(int code, const char* who, const char* why) {
   snprintf(msg, sizeof msg, "%s: %s", who, why);
   set_last_error(msg);
   return code;
+}
+
+int device_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];   // 0: not asked yet
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < kDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 int kv4_check(const mk_kv4_cache* c, const char* who) {
@@ -623,7 +635,7 @@ extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const
   if (int rc = kv4_check(cache, who)) return rc;
   const int esz = dtype_bytes(dtype);
   if (!esz) return kv4_fail(MK_ERR_INVALID_ARG, who, "dtype is one of MK_DTYPE_*");
-  if (n_tokens < 0) return kv4_fail(MK_ERR_INVALID_ARG, who, "n_tokens is not negative");
+  if (n_tokens < 0 || n_tokens > 1 << 30) return kv4_fail(MK_ERR_INVALID_ARG, who, "n_tokens is 0 to 2^30");
   if (!offsets_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no offsets");
   if (n_tokens == 0) return MK_OK;
   if (!k_dev || !v_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no keys or values");
@@ -636,10 +648,8 @@ extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const
   const Kv4 c = kv4_of(cache);
   const int per = c.heads * (cache->head_dim / kKv4Group);   // threads of a token
   const int at_once = per < kAppendThreads ? kAppendThreads / per : 1, cuts = (per + kAppendThreads - 1) / kAppendThreads;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return kv4_fail(MK_ERR_CUDA, who, "no device");
+  const int sms = device_sms();
+  if (!sms) return kv4_fail(MK_ERR_CUDA, who, "no device");
   const int wave = (dtype == MK_DTYPE_F32 ? 3 : 4) * sms;
   long long blocks = ((long long)n_tokens + at_once - 1) / at_once * cuts;
   if (blocks > wave) blocks = wave > cuts ? wave / cuts * cuts : cuts;

@@ -97,6 +97,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 // Checks an mk_kv4_cache; 0 or an MK_ERR_* code, with the reason in
 // mk_last_error(NULL).  `who` names the entry point.
 int kv4_check(const mk_kv4_cache* c, const char* who);
+// SMs of the current device (asked for once a device), 0 without one.
+int device_sms();
 int kv4_fail(int code, const char* who, const char* why);
 Kv4 kv4_of(const mk_kv4_cache* c);
 

@@ -1082,17 +1082,15 @@ extern "C" int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, in
   if ((reinterpret_cast<uintptr_t>(q_dev) & 15u) || (q_stride * esz) % 16 ||
       (reinterpret_cast<uintptr_t>(out_dev) & 15u))
     return kv4_fail(MK_ERR_INVALID_ARG, who, "queries of a token and the outputs are 16-byte aligned");
-  if (!(scale > 0.f) || !(scale <= 3.0e38f)) return kv4_fail(MK_ERR_INVALID_ARG, who, "scale is positive and finite");
+  if (!(scale >= 1e-18f) || !(scale <= 1e18f)) return kv4_fail(MK_ERR_INVALID_ARG, who, "scale is 1e-18 to 1e18");
   if (accumulate && !cache->scores_dev)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "weights are added to a cache's scores, and this one has none");
   const int group = n_q_heads / cache->n_kv_heads;
   const Layout l = layout_of(cache, dtype, q_len, group, accumulate != 0);
   if (!workspace_dev || (reinterpret_cast<uintptr_t>(workspace_dev) & 15u) || workspace_bytes < l.bytes)
     return kv4_fail(MK_ERR_INVALID_ARG, who, "the workspace is 16-byte aligned and of the bytes asked for");
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return kv4_fail(MK_ERR_CUDA, who, "no device");
+  const int sms = device_sms();
+  if (!sms) return kv4_fail(MK_ERR_CUDA, who, "no device");
   uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
   AttnArgs a;
   a.c = kv4_of(cache);

@@ -218,6 +218,19 @@ def test_reorder_of_segments_that_hold_all_beams(cuda_ok):
     assert torch.equal(t.cpu(), state[:, par[0].long()])
 
 
+def test_reorder_of_states_past_32_bits(cuda_ok):
+    size = 1 << 30
+    state = torch.zeros(3, 2, 1, size, dtype=torch.uint8, device="cuda")      # 6 GB
+    for r in range(3):
+        for i in range(2):
+            state[r, i, 0, :64] = 10 * r + i
+            state[r, i, 0, -64:] = 100 + 10 * r + i
+    binding.beam_reorder(state, torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"), 0, 1)
+    for r, p in enumerate((2, 0, 1)):
+        for i in range(2):
+            assert (state[r, i, 0, :64] == 10 * p + i).all() and (state[r, i, 0, -64:] == 100 + 10 * p + i).all()
+
+
 @pytest.mark.parametrize("dim,page,paged,scores", [(64, 32, True, True), (128, 96, True, False), (64, 128, False, True)])
 def test_kv4_reorder_moves_blocks_and_scores(cuda_ok, dim, page, paged, scores):
     n, W, heads, per = 2, 3, 2, 3

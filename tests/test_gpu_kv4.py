@@ -82,6 +82,7 @@ def _check(p, lens, q, out, scale, scores=None, before=None, skip=()):
 @pytest.mark.parametrize("heads,dim,page,counts,old", [
     (1, 64, 32, [1], [0]), (2, 64, 64, [1, 1, 1], [31, 32, 63]), (8, 128, 64, [5, 0, 70], [3, 9, 0]),
     (3, 128, 96, [100, 1], [0, 95]), (2, 64, 32, [0, 0, 33, 0], [1, 2, 3, 4]),
+    (33, 64, 32, [3, 2], [0, 31]), (40, 128, 32, [1, 3], [5, 0]), (1, 64, 32, [1] * 600, [i % 7 for i in range(600)]),
 ])
 def test_append_writes_the_format(cuda_ok, dtype, heads, dim, page, counts, old):
     lens = [a + b for a, b in zip(old, counts)]
@@ -208,7 +209,8 @@ def test_read_gives_the_values_and_leaves_the_rest(cuda_ok, dtype, dim, page):
     ([700, 65, 1, 2049], 8, 4, 128, 1, 64, True), ([5], 1, 16, 128, 1, 32, True),
     ([3, 0, 40, 129], 2, 4, 128, 5, 32, True), ([40, 7], 1, 9, 64, 3, 64, True),
     ([64, 96], 3, 5, 64, 8, 96, True), ([2], 1, 8, 128, 16, 32, True), ([300], 1, 1, 64, 33, 64, True),
-    ([257] * 40, 1, 2, 64, 1, 32, True), ([0, 0], 2, 2, 64, 2, 32, True),
+    ([257] * 40, 1, 2, 64, 1, 32, True), ([0, 0], 2, 2, 64, 2, 32, True), ([90, 3], 2, 4, 128, 10, 32, True),
+    ([i % 5 * 9 for i in range(700)], 1, 1, 64, 1, 64, True), ([100, 33], 1, 8, 128, 3, 64, False),
 ])
 def test_attention_matches_the_reference(cuda_ok, dtype, lens, heads, group, dim, q_len, page, acc):
     p = Plain(len(lens), heads, dim, page, -(-max(max(lens), 1) // page), seed=len(lens), k_log2=1, v_log2=-1)
@@ -363,6 +365,209 @@ def test_attention_strided_queries_and_one_page_without_table(cuda_ok):
     binding.attention_kv4(bare, q, out, _workspace(bare, 2, 4, False))
     _check(p, lens, q, out, 0.125)
     assert torch.equal(out, _attend(c, q.contiguous()))
+
+
+def test_addresses_that_are_only_16_byte_aligned(cuda_ok):
+    """Rows 16 bytes off a 32-byte boundary, in and out."""
+    for dtype in TYPES.values():
+        off = 16 // torch.empty((), dtype=dtype).element_size()
+        p = Plain(1, 2, 64, 32, 2, seed=1)
+        c = _cuda(p, [50])
+        raw = torch.randn(2, 50 * 128 + off, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+        k, v = (x[off:].view(50, 2, 64) for x in raw)
+        assert k.data_ptr() % 32 == 16
+        binding.kv4_append(c, k, v, torch.tensor([0, 50], dtype=torch.int32, device="cuda"))
+        for j in range(50):
+            p.write(0, j, k[j].double().cpu().numpy(), v[j].double().cpu().numpy())
+        assert np.array_equal(c.pool.cpu().numpy(), p.pool)
+        back = torch.zeros(2, 50 * 128 + off, dtype=dtype, device="cuda")
+        ko, vo = (x[off:].view(1, 50, 2, 64) for x in back)
+        binding.kv4_read(c, ko, vo)
+        for x, y in zip((ko, vo), p.read(0, 50)):
+            assert np.array_equal(x[0].double().cpu().numpy(), y)
+        q = torch.randn(2 * 64 + off, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()[off:].view(1, 1, 2, 64)
+        out = torch.zeros(2 * 64 + off, dtype=dtype, device="cuda")[off:].view(1, 1, 2, 64)
+        _check(p, [50], q, _attend(c, q, out=out), 0.125)
+
+
+def test_pools_past_32_bits(cuda_ok):
+    """Pages whose bytes lie 5 GB into the pool, through every operator."""
+    heads, dim, page, pages = 8, 128, 64, 70000
+    size = heads * page * (dim + dim // 8)
+    pool = torch.zeros(pages, size, dtype=torch.uint8, device="cuda")
+    table = torch.tensor([[pages - 1, 60000], [65000, 2]], dtype=torch.int32, device="cuda")
+    lens = [100, 70]
+    p = Plain(2, heads, dim, page, 2, seed=1)
+    p.table = np.array([[0, 1], [2, 3]], np.int32)
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(2, 170, heads, dim, generator=g)
+    for s, a in ((0, 0), (1, 100)):
+        for j in range(lens[s]):
+            p.write(s, j, x[0, a + j].double().numpy(), x[1, a + j].double().numpy())
+    scores = torch.zeros(2, heads, 128, device="cuda")
+    c = binding.Kv4Cache(pool, torch.tensor(lens, dtype=torch.int32, device="cuda"), heads, dim, page, table, scores)
+    k, v = x.cuda()
+    binding.kv4_append(c, k, v, torch.tensor([0, 100, 170], dtype=torch.int32, device="cuda"))
+    assert np.array_equal(pool[table.view(-1).long()].cpu().numpy(), p.pool)
+    q = torch.randn(2, 1, 32, dim, generator=g).cuda()
+    out = _attend(c, q, True)
+    _check(p, lens, q, out, dim ** -0.5, scores, np.zeros((2, heads, 128)))
+    dst_table = torch.tensor([[69998], [69997]], dtype=torch.int32, device="cuda")
+    dst = binding.Kv4Cache(pool, torch.tensor([64, 64], dtype=torch.int32, device="cuda"), heads, dim, page, dst_table,
+                           torch.zeros(2, heads, 64, device="cuda"))
+    kept = torch.zeros(2, heads, 64, dtype=torch.int32, device="cuda")
+    before = scores.cpu().numpy()
+    binding.kv4_evict(c, dst, 64, 4, 8, kept)
+    ko = torch.zeros(2, 64, heads, dim, device="cuda")
+    vo = torch.zeros_like(ko)
+    binding.kv4_read(dst, ko, vo)
+    for s in range(2):
+        a, b = p.read(s, lens[s])
+        for h in range(heads):
+            want = _kept(before[s, h], lens[s], 64, 4, 8)
+            assert kept[s, h].tolist() == want
+            assert np.array_equal(ko[s, :, h].double().cpu().numpy(), a[want, h])
+            assert np.array_equal(vo[s, :, h].double().cpu().numpy(), b[want, h])
+    par = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    old = pool[dst_table.view(-1).long()].clone()
+    binding.kv4_reorder(dst, par, 0, 64)
+    assert torch.equal(pool[dst_table.view(-1).long()], old.flip(0))
+
+
+def test_attention_over_millions_of_keys(cuda_ok):
+    """One head's 2.6 million keys in small pages: a warp's range runs over more
+    pages than it looks up at once.  Against 64 bits on the values read back."""
+    n, dim, page = 2_600_001, 64, 32
+    pages = -(-n // page)
+    pool = torch.randint(0, 256, (pages, page * (dim + dim // 8)), dtype=torch.uint8, device="cuda",
+                         generator=torch.Generator("cuda").manual_seed(1))
+    half = page * (dim // 2 + dim // 16)
+    blocks = pool.view(pages, 2, half)
+    blocks[:, :, page * dim // 2:] = blocks[:, :, page * dim // 2:] % 8 + 40      # scales 1/4 to 1/2
+    table = torch.randperm(pages, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).int().view(1, -1)
+    c = binding.Kv4Cache(pool, torch.tensor([n], dtype=torch.int32, device="cuda"), 1, dim, page, table,
+                         torch.zeros(1, 1, pages * page, device="cuda"))
+    q = torch.randn(1, 1, 2, dim, generator=torch.Generator().manual_seed(3)).cuda()
+    out = _attend(c, q, True)
+    k = torch.zeros(1, n, 1, dim, device="cuda")
+    v = torch.zeros_like(k)
+    binding.kv4_read(c, k, v)
+    kd, vd, qd = k[0, :, 0].double(), v[0, :, 0].double(), q[0, 0].double()
+    w = torch.softmax(qd @ kd.T / 8, -1)
+    want, mass = w @ vd, w @ vd.abs()
+    reach = (qd.abs() @ kd.abs().T).amax(-1) / 8
+    tol = _bound(want.cpu().numpy(), mass.cpu().numpy(), reach.cpu().numpy(), q.dtype)
+    # fp32 sums over 2.6 million keys: 1,100 additions a thread, then 28 partials
+    tol = tol + mass.cpu().numpy() * 1200 * 2.0 ** -24
+    assert (np.abs((out[0, 0].double() - want).cpu().numpy()) <= tol).all()
+    t = 4 * 2.0 ** -18 * float(reach.max()) + 2.0 ** -17 + 1200 * 2.0 ** -24
+    assert ((c.scores[0, 0, :n].double() - w.sum(0)).abs() <= w.sum(0) * t + 1e-30).all()
+
+
+def test_every_operator_is_replayed_from_a_graph(cuda_ok):
+    """Append, attention, eviction and reading captured together, replayed with
+    other contents, lengths and offsets."""
+    p = Plain(2, 2, 64, 32, 3, seed=5)
+    c = _cuda(p, [0, 0], np.zeros((2, 2, 96)))
+    d = Plain(2, 2, 64, 32, 1, seed=6)
+    dst = _cuda(d, [0, 0], np.zeros((2, 2, 32)))
+    k, v = torch.zeros(2, 120, 2, 64, device="cuda")
+    offs = torch.zeros(3, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 1, 4, 64, generator=torch.Generator().manual_seed(3)).cuda()
+    out, ws = torch.zeros_like(q), _workspace(c, 1, 4, True)
+    kept = torch.zeros(2, 2, 32, dtype=torch.int32, device="cuda")
+    ko, vo = torch.zeros(2, 2, 32, 2, 64, device="cuda")
+
+    def step():
+        binding.kv4_append(c, k, v, offs)
+        binding.attention_kv4(c, q, out, ws, accumulate=True)
+        binding.kv4_evict(c, dst, 32, 2, 3, kept)
+        binding.kv4_read(dst, ko, vo)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed, lens in ((1, [60, 60]), (2, [96, 0]), (3, [5, 33])):
+        x = torch.randn(2, 120, 2, 64, generator=torch.Generator().manual_seed(seed))
+        k.copy_(x[0])
+        v.copy_(x[1])
+        offs.copy_(torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32))
+        c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        dst.lens.copy_(torch.tensor(lens, dtype=torch.int32).clamp(max=32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, a in ((0, 0), (1, lens[0])):
+            for j in range(lens[s]):
+                p.write(s, j, x[0, a + j].double().numpy(), x[1, a + j].double().numpy())
+        _check(p, lens, q, out, 0.125)
+        weights = c.scores.cpu().numpy()
+        for s, n in enumerate(lens):
+            a, b = p.read(s, n)
+            for h in range(2):
+                want = _kept(weights[s, h], n, 32, 2, 3)
+                assert kept[s, h].tolist() == want + [-1] * (32 - len(want))
+                assert np.array_equal(ko[s, :len(want), h].double().cpu().numpy(), a[want, h])
+                assert np.array_equal(vo[s, :len(want), h].double().cpu().numpy(), b[want, h])
+
+
+def test_evict_and_append_twice_at_once(cuda_ok):
+    """The same call on two streams, caches of their own."""
+    n = 9000
+    rng = np.random.default_rng(2)
+    scores = np.exp(rng.normal(size=(1, 4, 9024)))
+    p = Plain(1, 4, 64, 32, 282, seed=1)
+    p.fill_random([n])
+    src = [_cuda(p, [n], scores) for _ in range(2)]
+    d = Plain(1, 4, 64, 32, 32, seed=2)
+    dst = [_cuda(d, [1000], np.zeros((1, 4, 1024))) for _ in range(2)]
+    kept = [torch.zeros(1, 4, 1000, dtype=torch.int32, device="cuda") for _ in range(2)]
+    x = torch.randn(2, 1000, 4, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    offs = torch.tensor([0, 1000], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(2):
+        st = torch.cuda.Stream()
+        for _ in range(3):
+            binding.kv4_append(src[i], x[0], x[1], offs, stream=st)
+            binding.kv4_evict(src[i], dst[i], 1000, 4, 32, kept[i], stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(kept[0], kept[1]) and torch.equal(dst[0].pool, dst[1].pool)
+    sc = src[0].scores.cpu().numpy()
+    for h in range(4):
+        assert kept[0][0, h].tolist() == _kept(sc[0, h], n, 1000, 4, 32)
+
+
+def test_the_binding_refuses_other_tensors(cuda_ok):
+    pool = torch.zeros(4, binding.kv4_page_bytes(2, 64, 32), dtype=torch.uint8, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad, err in ((dict(pool=pool.cpu()), TypeError), (dict(lens=lens.long()), TypeError), (dict(pool=pool[:3]), ValueError),
+                     (dict(pool=pool[:, :-1]), ValueError), (dict(head_dim=96), binding.MkError),
+                     (dict(scores=torch.zeros(2, 2, 63, device="cuda")), ValueError),
+                     (dict(table=torch.zeros(3, 2, dtype=torch.int32, device="cuda")), ValueError)):
+        kw = dict(pool=pool, lens=lens, n_kv_heads=2, head_dim=64, page_tokens=32)
+        kw.update(bad)
+        with pytest.raises(err):
+            binding.Kv4Cache(**kw)
+    c = binding.Kv4Cache(pool, lens, 2, 64, 32)
+    k = torch.zeros(3, 2, 64, device="cuda")
+    offs = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for args in ((k, k[:2], offs), (k, k.half(), offs), (k[:, :1], k[:, :1], offs), (k, k, offs[:2]), (k.cpu(), k, offs),
+                 (k.transpose(1, 2), k, offs)):
+        with pytest.raises(ValueError):
+            binding.kv4_append(c, *args)
+    with pytest.raises(TypeError):
+        binding.kv4_append(c, k.double(), k.double(), offs)
+    q = torch.zeros(2, 1, 4, 64, device="cuda")
+    ws = _workspace(c, 1, 4, False)
+    for args in ((q[:1], q[:1], ws), (q, q[:, :, :2], ws), (q.transpose(2, 3), q, ws)):
+        with pytest.raises((ValueError, TypeError)):
+            binding.attention_kv4(c, *args)
+    with pytest.raises(TypeError):
+        binding.attention_kv4(c, q, torch.zeros_like(q).half(), ws)
+    with pytest.raises(binding.MkError):                      # a workspace that is too small
+        binding.attention_kv4(c, q, torch.zeros_like(q), ws[:4096])
+    with pytest.raises(binding.MkError):                      # no scores to add to
+        binding.attention_kv4(c, q, torch.zeros_like(q), _workspace(c, 1, 4, True), accumulate=True)
 
 
 def test_attention_repeats_bit_for_bit_on_other_streams_and_workspaces(cuda_ok):

@@ -55,7 +55,7 @@ def test_no_cache():
 
 
 @pytest.mark.parametrize("args,part", [
-    ((A, A, 3, 128, 128, A, 1), "dtype"), ((A, A, 0, 128, 128, A, -1), "n_tokens"), ((A, A, 0, 128, 128, None, 1), "offsets"),
+    ((A, A, 3, 128, 128, A, 1), "dtype"), ((A, A, 0, 128, 128, A, -1), "n_tokens"), ((A, A, 0, 128, 128, A, (1 << 30) + 1), "n_tokens"), ((A, A, 0, 128, 128, None, 1), "offsets"),
     ((None, A, 0, 128, 128, A, 1), "keys"), ((A, None, 0, 128, 128, A, 1), "keys"), ((A, A, 0, 127, 128, A, 1), "stride"),
     ((A, A, 0, 128, 64, A, 1), "stride"), ((A + 4, A, 0, 128, 128, A, 1), "aligned"), ((A, A, 1, 132, 128, A, 1), "aligned"),
     ((A, A, 0, 128, 130, A, 1), "aligned"),
@@ -88,7 +88,7 @@ def test_read_refuses(args, part):
     (dict(dtype=3), "dtype"), (dict(q=None), "queries"), (dict(out=None), "queries"), (dict(stride=255), "stride"),
     (dict(q=A + 8), "aligned"), (dict(dtype=1, stride=260), "aligned"), (dict(out=A + 2), "aligned"),
     (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"),
-    (dict(scale=float("inf")), "scale"), (dict(ws=None), "workspace"), (dict(ws=A + 4), "workspace"),
+    (dict(scale=float("inf")), "scale"), (dict(scale=1e-19), "scale"), (dict(scale=2e18), "scale"), (dict(ws=None), "workspace"), (dict(ws=A + 4), "workspace"),
     (dict(size=-1), "workspace"),
 ])
 def test_attention_refuses(change, part):
