@@ -243,6 +243,7 @@ def prefill_graph(model, T: int, tiles, lm_req, num_ctas: int):
 
 class Plan:
     """The task graph mk_create would build (host only)."""
+
     def __init__(self, model, max_seq: int, num_ctas: int, max_batch: int = 1,
                  attn_splits: int = 0, weight_format: int = 0):
         L = lib()
@@ -292,6 +293,7 @@ def qkv_row_source(model, r: int):
 class Decoder:
     """One libmk context.  ``weights`` maps the synthetic generator's names to
     CUDA bf16 tensors; mk_create copies them, so they may be dropped after."""
+
     def __init__(self, model, weights: Dict[str, "torch.Tensor"], max_seq: int,
                  max_batch: int = 1, num_ctas: int = 0, attn_splits: int = 0,
                  timeout_ms: int = 0, mode: int = MODE_MEGAKERNEL, stream=None,
@@ -578,6 +580,7 @@ class Kv4Cache:
     ``scores`` fp32 [n_seq, n_kv_heads, pages_per_seq * page_tokens] or None.
     Holds the tensors, copies nothing; their contents may change between
     calls, their storage not."""
+
     def __init__(self, pool, lens, n_kv_heads: int, head_dim: int, page_tokens: int, table=None,
                  scores=None, k_log2: int = 0, v_log2: int = 0):
         page = lib().mk_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
