@@ -636,7 +636,8 @@ extern "C" int mk_kv4_append(const mk_kv4_cache* cache, const void* k_dev, const
   const int esz = dtype_bytes(dtype);
   if (!esz) return kv4_fail(MK_ERR_INVALID_ARG, who, "dtype is one of MK_DTYPE_*");
   if (n_tokens < 0 || n_tokens > 1 << 30) return kv4_fail(MK_ERR_INVALID_ARG, who, "n_tokens is 0 to 2^30");
-  if (!offsets_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no offsets");
+  if (!offsets_dev || (reinterpret_cast<uintptr_t>(offsets_dev) & 3u))
+    return kv4_fail(MK_ERR_INVALID_ARG, who, "offsets are a 4-byte aligned array");
   if (n_tokens == 0) return MK_OK;
   if (!k_dev || !v_dev) return kv4_fail(MK_ERR_INVALID_ARG, who, "no keys or values");
   const long long row = (long long)cache->n_kv_heads * cache->head_dim;

@@ -65,6 +65,11 @@ def test_append_refuses(args, part):
     _refused(binding.lib().mk_kv4_append(C.addressof(c), *args, None), -1, part)
 
 
+def test_append_refuses_offsets_between_words():
+    c = _cache()
+    _refused(binding.lib().mk_kv4_append(C.addressof(c), A, A, 0, 128, 128, A + 2, 1, None), -1, "offsets")
+
+
 def test_empty_calls_are_no_errors():
     L, c = binding.lib(), _cache()
     r = C.addressof(c)
