@@ -742,6 +742,6 @@ def beam_reorder(state, parents, first: int, count: int, stream=None):
         raise ValueError("positions [first, first + count) of the state")
     if count == 0 or state.numel() == 0:
         return
-    row = state.element_size() * state.stride(2)
+    row = state.nbytes // (state.shape[0] * segments * positions)   # not a stride: of one position it may be anything
     _on(d, stream, lib().mk_beam_reorder, base + first * row, _tensor(parents, torch.int32, "parents", None, d),
         parents.shape[0], parents.shape[1], segments * positions * row, segments, positions * row, count * row)

@@ -2,8 +2,10 @@
 device (addresses here are never dereferenced), and their sizes are what the
 format says."""
 import ctypes as C
+import math
 
 import pytest
+import torch
 
 from persistent_megakernel_03_b200 import binding
 
@@ -179,6 +181,23 @@ def test_reorder_refuses(change, part):
     f.update(change)
     _refused(binding.lib().mk_beam_reorder(f["state"], f["par"], f["n"], f["beams"], f["beam"], f["segs"], f["seg"],
                                            f["size"], None), -1, part)
+
+
+@pytest.mark.parametrize("shape,strides", [
+    ((4, 2, 3, 8), (48, 24, 8, 1)), ((4, 1, 1, 16), (16, 999, 777, 1)), ((4, 1, 1, 16), (16, 1, 1, 1)),
+    ((4, 3, 1, 16), (48, 16, 4096, 1)), ((4, 1, 5), (5, 64, 1))])
+def test_binding_reorder_goes_by_shape(shape, strides, monkeypatch):
+    """The stride of an axis of one entry means nothing: such a tensor is contiguous."""
+    seen = []
+    monkeypatch.setattr(binding, "_tensor", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(binding, "_on", lambda device, stream, call, *a: seen.append(a))
+    state = torch.empty(200).as_strided(shape, strides)
+    assert state.is_contiguous()
+    n = shape[2]
+    binding.beam_reorder(state, torch.zeros(2, 2, dtype=torch.int32), n - 1, 1)
+    row = 4 * math.prod(shape[3:])
+    assert seen[0][0] == state.data_ptr() + (n - 1) * row
+    assert seen[0][2:] == (2, 2, shape[1] * n * row, shape[1], n * row, row)
 
 
 def test_reorder_takes_beams_inside_segments():
