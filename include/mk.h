@@ -377,9 +377,10 @@ int mk_attention_decode_noalloc(const float* q_dev, const void* k_dev, const voi
  * to the next and can be captured into a graph.  Argument errors return before
  * anything is enqueued, with the reason in mk_last_error(NULL); sizes and
  * indices that only the device sees (lengths, pages, parents) are checked
- * there and cut or skipped as each operator says.  Results do not depend on
- * timing: no operator uses atomics.  Calls that overlap on the GPU need
- * workspaces of their own.
+ * there and cut or skipped as each operator says, and must not change while a
+ * call that reads them is in flight.  Results do not depend on timing: the
+ * only atomics are counts.  Calls that overlap on the GPU need workspaces of
+ * their own.
  */
 #define MK_DTYPE_F32 0
 #define MK_DTYPE_BF16 1

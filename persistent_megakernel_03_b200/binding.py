@@ -406,7 +406,7 @@ class Decoder:
         log-probabilities [beams] fp32).  Sequences that reached ``eos`` (>= 0)
         go on with it.  Uses slots 0..beams-1; after the prefill, steps,
         selection and the caches' reordering are enqueued without a host round
-        trip."""
+        trip, all on the decoder's stream, whose work the results are."""
         if not 1 <= beams <= self.max_batch:
             raise ValueError("beams is 1 to max_batch")
         n, V, dev = prompt_dev.numel(), self.model.vocab, prompt_dev.device
