@@ -441,8 +441,7 @@ int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, vo
  * query heads: token i of sequence s sees slots j < lens[s] - q_len + i + 1
  * (its own key included), out = softmax(scale * q k^T) v.  q_dev: `dtype`
  * [n_seq * q_len][n_q_heads][head_dim], tokens q_stride elements apart, 16-byte
- * aligned, finite (a row that is not gets NaN or infinities, the others stay
- * right); query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
+ * aligned, finite (a row that is not gets NaN, the others stay right); query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
  * n_q_heads / n_kv_heads <= 1024; 1e-18 <= scale <= 1e18.  out_dev: the same type,
  * [n_seq][q_len][n_q_heads][head_dim], 16-byte aligned.  fp32 softmax and sums; queries and
  * probabilities enter the products with at least 22 bits (probabilities of a

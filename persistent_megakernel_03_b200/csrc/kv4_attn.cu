@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       // 2^e with max |q| * 2^e in [2^13, 2^14); the exponent kept inside fp32's own
       int e = 13 - ((__float_as_int(top) >> 23) - 127);
       e = min(max(e, -120), 120);
-      const float up = __int_as_float((127 + e) << 23);
+      // A row with an infinity becomes NaN, as one with a NaN is: scores that were all
+      // -inf would pass for those of a row that sees nothing.
+      const float up = top <= 3.402823466e38f ? __int_as_float((127 + e) << 23) : __int_as_float(0x7FC00000);
       // not 0: masked scores are -inf and their product has to stay it
       const float down = fmaxf(__int_as_float((127 - e) << 23) * a.s_mul, 1.17549435e-38f);
 #pragma unroll

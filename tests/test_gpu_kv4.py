@@ -329,6 +329,24 @@ def test_attention_nan_reaches_only_rows_that_see_it(cuda_ok, dim, group, dtype)
     assert (np.abs(out[0].double().cpu().numpy() - o)[ok] <= _bound(o, mass, reach, q.dtype)[ok]).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,n", [(64, 3), (128, 700)])
+def test_attention_row_of_minus_infinities_is_not_an_empty_one(cuda_ok, dim, n, dtype):
+    """An infinite query against keys of one sign: every score is -inf, and the
+    softmax of that is NaN, not the zeros of a row that sees nothing."""
+    k = -torch.ones(n, 1, dim)
+    p = Plain(1, 1, dim, 32, -(-n // 32), seed=1)
+    c = _cuda(p, [n])
+    binding.kv4_append(c, k.cuda(), torch.ones(n, 1, dim).cuda(), torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    q = torch.zeros(1, 1, 2, dim)
+    q[0, 0, 1] = float("inf")
+    out = _attend(c, q.to(TYPES[dtype]).cuda())
+    assert torch.isnan(out[0, 0, 1]).all()
+    # 1/6 is nearest 11/64: ones read back as 6 * 11/64; a mean of equal values
+    want = torch.full((dim,), 1.03125)
+    assert ((out[0, 0, 0].float().cpu() - want).abs() <= 1.03125 * (torch.finfo(TYPES[dtype]).eps / 2 + PART[TYPES[dtype]] + 2.0 ** -18)).all()
+
+
 def test_attention_small_weights_add_up(cuda_ok):
     """One key far above thousands of equal ones: each of their weights is 2^-20
     of the first, together they are not."""
