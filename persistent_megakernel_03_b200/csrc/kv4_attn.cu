@@ -940,9 +940,11 @@ __global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const Attn
         if (lane == 0) stat[row] = make_float2(m == -INFINITY ? 0.f : kBias - m, l != 0.f ? 1.f / l : 0.f);
       }
       __syncthreads();
+      // a key that a row does not see has score -inf; the row's sum may be NaN, so the
+      // product would not always be 0
       auto weigh = [&](float w, float2 x, int row) {
-        if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
-        if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
+        if (row < a.rows && x.x != -INFINITY) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
+        if (row + 1 < a.rows && x.y != -INFINITY) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
         return w;
       };
 #pragma unroll

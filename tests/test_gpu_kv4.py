@@ -329,6 +329,40 @@ def test_attention_nan_reaches_only_rows_that_see_it(cuda_ok, dim, group, dtype)
     assert (np.abs(out[0].double().cpu().numpy() - o)[ok] <= _bound(o, mass, reach, q.dtype)[ok]).all()
 
 
+def _with_bad_row(cuda_ok, dtype, dim, group, n, bad):
+    """Token 1 of 4 has one query head with a bad element: (plain cache, clean
+    queries, cache with scores, outputs)."""
+    p = Plain(1, 2, dim, 32, -(-n // 32), seed=7)
+    p.fill_random([n])
+    q = torch.randn(1, 4, 2 * group, dim, generator=torch.Generator().manual_seed(6)).to(TYPES[dtype])
+    q[0, 1, 0] = 0
+    dirty = q.clone()
+    dirty[0, 1, 0, 5] = bad
+    c = _cuda(p, [n], np.zeros((1, 2, p.capacity)))
+    return p, q, c, _attend(c, dirty.cuda(), True)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,group,n", [(64, 1, 45), (128, 4, 2003), (64, 9, 300)])
+def test_attention_bad_query_row_stays_alone(cuda_ok, dim, group, n, dtype, bad):
+    """A NaN or an infinity in one query row: that row is NaN and so are the
+    scores of the keys that it sees; other rows, and the keys that only later
+    tokens see, are as without it."""
+    p, q, c, out = _with_bad_row(cuda_ok, dtype, dim, group, n, bad)
+    nan = torch.isnan(out[0]).cpu()
+    assert nan[1, 0].all() and int(nan.sum()) == dim
+    k, v = p.read(0, n)
+    want, w, mass, reach = attend(q[0].double().numpy(), k, v, dim ** -0.5, group)
+    ok = ~nan.numpy()
+    assert (np.abs(out[0].double().cpu().numpy() - want)[ok] <= _bound(want, mass, reach, q.dtype)[ok]).all()
+    got = c.scores[0, :, :n].double().cpu().numpy()
+    assert np.isnan(got[0, :n - 2]).all()
+    t = 4 * 2.0 ** -18 * reach.max() + 2.0 ** -17
+    for a, b in ((got[0, n - 2:], w[0, n - 2:]), (got[1], w[1])):
+        assert (np.abs(a - b) <= b * t + b * 2.0 ** -22 + 1e-30).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim,n", [(64, 3), (128, 700)])
 def test_attention_row_of_minus_infinities_is_not_an_empty_one(cuda_ok, dim, n, dtype):
