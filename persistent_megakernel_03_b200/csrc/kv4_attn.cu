@@ -233,6 +233,11 @@ __device__ __forceinline__ bool out_row(const AttnArgs& a, int seq, int tile, in
 // has sum 0, NaN goes through.
 __device__ __forceinline__ float inverse(const AttnArgs& a, float sum) { return sum == 0.f ? 0.f : a.o_mul / sum; }
 
+// What is added to a score to get its probability's exponent.  Rounded down: with a reference
+// past 2^24 the bias goes (the nearest step of fp32 could be 16 above it), and a
+// probability stays below 2^16.  No reference yet: nothing is added.
+__device__ __forceinline__ float exponent_of(float ref) { return ref == -INFINITY ? 0.f : __fadd_rd(kBias, -ref); }
+
 // Weight of a partial with maximum mi under the common maximum m.
 __device__ __forceinline__ float rescale(float mi, float m) {
   return mi == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mi - m);
@@ -417,8 +422,11 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       // A row with an infinity becomes NaN, as one with a NaN is: scores that were all
       // -inf would pass for those of a row that sees nothing.
       const float up = top <= 3.402823466e38f ? __int_as_float((127 + e) << 23) : __int_as_float(0x7FC00000);
-      // not 0: masked scores are -inf and their product has to stay it
-      const float down = fmaxf(__int_as_float((127 - e) << 23) * a.s_mul, 1.17549435e-38f);
+      // not 0: masked scores are -inf and their product has to stay it; at most 2^94:
+      // a product q k is below 2^33 (14 + 11.4 + 7 bits), so no score passes fp32's range.
+      // What is cut still tells scores apart: they are multiples of 2^-34, and 2^60 log2 units
+      // are as good as any number of them.
+      const float down = fminf(fmaxf(__int_as_float((127 - e) << 23) * a.s_mul, 1.17549435e-38f), 1.9807040628566084e28f);
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) {
         const float f0 = x[2 * i] * up, f1 = x[2 * i + 1] * up;
@@ -570,8 +578,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          top[nt][c] = mul[nt][c] * fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
-          moves |= top[nt][c] > ref[nt][c] + kSlack;
+          top[nt][c] = __fmul_rn(mul[nt][c], fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), fmaxf(sc[1][nt][c], sc[1][nt][2 + c])));
+          moves |= top[nt][c] - ref[nt][c] > kSlack;
         }
       if (__any_sync(0xFFFFFFFFu, moves)) {
 #pragma unroll
@@ -595,14 +603,15 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       uint32_t pf[PP][2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = ref[nt][0] == -INFINITY ? 0.f : kBias - ref[nt][0];
-        const float m1 = ref[nt][1] == -INFINITY ? 0.f : kBias - ref[nt][1];
+        // Scores are rounded before the reference is taken off, as the reference was: one
+        // fma would keep bits that the reference has lost, many log2 units of a large score.
+        const float m0 = exponent_of(ref[nt][0]), m1 = exponent_of(ref[nt][1]);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = ex2(fmaf(sc[half][nt][2 * i], mul[nt][0], m0));
-            const float p1 = ex2(fmaf(sc[half][nt][2 * i + 1], mul[nt][1], m1));
+            const float p0 = ex2(__fadd_rn(__fmul_rn(sc[half][nt][2 * i], mul[nt][0]), m0));
+            const float p1 = ex2(__fadd_rn(__fmul_rn(sc[half][nt][2 * i + 1], mul[nt][1]), m1));
             sum[nt][0] += p0;
             sum[nt][1] += p1;
             const uint32_t h = pack_half2(p0, p1);
@@ -937,14 +946,14 @@ __global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const Attn
             join(m, l, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, l, o));
         }
         // sums carry the bias of the probabilities
-        if (lane == 0) stat[row] = make_float2(m == -INFINITY ? 0.f : kBias - m, l != 0.f ? 1.f / l : 0.f);
+        if (lane == 0) stat[row] = make_float2(exponent_of(m), l != 0.f ? 1.f / l : 0.f);
       }
       __syncthreads();
       // a key that a row does not see has score -inf; the row's sum may be NaN, so the
       // product would not always be 0
       auto weigh = [&](float w, float2 x, int row) {
-        if (row < a.rows && x.x != -INFINITY) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
-        if (row + 1 < a.rows && x.y != -INFINITY) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
+        if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), x.x == -INFINITY ? 0.f : stat[row].y, w);
+        if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), x.y == -INFINITY ? 0.f : stat[row + 1].y, w);
         return w;
       };
 #pragma unroll

@@ -381,6 +381,32 @@ def test_attention_row_of_minus_infinities_is_not_an_empty_one(cuda_ok, dim, n, 
     assert ((out[0, 0, 0].float().cpu() - want).abs() <= 1.03125 * (torch.finfo(TYPES[dtype]).eps / 2 + PART[TYPES[dtype]] + 2.0 ** -18)).all()
 
 
+@pytest.mark.parametrize("dtype,scale,k_log2", [
+    ("fp32", 1.0, 0), ("bf16", 1.0, 0), ("fp32", 2.0 ** 59, 32), ("bf16", 2.0 ** 59, 32), ("fp16", 2.0 ** 59, 32),
+    ("fp32", 2.0 ** -59, 0)])
+@pytest.mark.parametrize("dim,n", [(64, 40), (128, 1500)])
+def test_attention_of_scores_past_fp32(cuda_ok, dim, n, dtype, scale, k_log2):
+    """Finite queries whose scores pass fp32's range: the highest key takes all
+    the weight (equal ones share it).  Queries and keys are powers of two times
+    few bits, so their products and sums are exact here: no error of the scores
+    enters the bound."""
+    p = Plain(1, 2, dim, 32, -(-n // 32), seed=3, k_log2=k_log2)
+    p.fill_random([n], size=1.0)
+    g = torch.Generator().manual_seed(dim)
+    top = 15 if dtype == "fp16" else 127
+    q = torch.where(torch.rand(1, 2, 6, dim, generator=g) < 0.5, 1.0, -1.0) * 2.0 ** (
+        top - torch.randint(0, 3, (1, 2, 6, dim), generator=g).float())
+    q = q.to(TYPES[dtype]).cuda()
+    assert torch.isfinite(q).all()
+    c = _cuda(p, [n], np.zeros((1, 2, p.capacity)))
+    out = _attend(c, q, True, scale)
+    k, v = p.read(0, n)
+    want, w, mass, _ = attend(q[0].double().cpu().numpy(), k, v, scale, 3)
+    tol = np.abs(want) * torch.finfo(q.dtype).eps / 2 + mass * (PART[q.dtype] + 2.0 ** -18) + 2.0 ** -25
+    assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
+    assert (np.abs(c.scores[0, :, :n].double().cpu().numpy() - w) <= w * 2.0 ** -17 + 1e-30).all()
+
+
 def test_attention_small_weights_add_up(cuda_ok):
     """One key far above thousands of equal ones: each of their weights is 2^-20
     of the first, together they are not."""
