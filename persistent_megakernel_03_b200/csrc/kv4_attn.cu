@@ -945,15 +945,15 @@ __global__ void __launch_bounds__(kThreadsM, 4) kv4_attn_merge_kernel(const Attn
           for (int o = 16; o; o >>= 1)
             join(m, l, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, l, o));
         }
-        // sums carry the bias of the probabilities
-        if (lane == 0) stat[row] = make_float2(exponent_of(m), l != 0.f ? 1.f / l : 0.f);
+        // Sums carry the bias of the probabilities.  No maximum: every score that the row sees is
+        // NaN (a bad query), or it sees none.  A factor of 1 then, as a NaN sum would spread to the
+        // keys that it does not see (score -inf, whose weight is 0).
+        if (lane == 0) stat[row] = make_float2(exponent_of(m), m == -INFINITY ? 1.f : 1.f / l);
       }
       __syncthreads();
-      // a key that a row does not see has score -inf; the row's sum may be NaN, so the
-      // product would not always be 0
       auto weigh = [&](float w, float2 x, int row) {
-        if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), x.x == -INFINITY ? 0.f : stat[row].y, w);
-        if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), x.y == -INFINITY ? 0.f : stat[row + 1].y, w);
+        if (row < a.rows) w = fmaf(ex2(x.x + stat[row].x), stat[row].y, w);
+        if (row + 1 < a.rows) w = fmaf(ex2(x.y + stat[row + 1].x), stat[row + 1].y, w);
         return w;
       };
 #pragma unroll
