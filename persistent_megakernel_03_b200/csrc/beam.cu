@@ -24,8 +24,9 @@ namespace {
 // ties make them too many, rounds over all logits find the lowest places.  A
 // second kernel, one CTA a search and one warp a beam, joins the chunks: the
 // log-sum-exp, the beam's W best (they lie in the W chunks with the highest
-// heads), then the best of W * W scores.  Scores are compared in 64 bits, so
-// that candidates of different beams are not ordered by rounding.
+// heads), then the best of W * W scores.  The chunks' sums are fp32 sums; where their
+// error could decide between candidates of two beams the join takes those beams' sums
+// again, in 64 bits and in no order, so candidates are never ordered by rounding.
 //
 // Bound: the logits' bytes once (4.1 MB for 8 beams of 128,256 in fp32: under
 // 1 us) beside two launches and W rounds of warp maxima in each.
@@ -74,7 +75,7 @@ struct SelectArgs {
   int32_t* parents;
   float* scores;
   uint8_t* done;              // null: not wanted
-  int32_t beams, vocab, chunks, eos;
+  int32_t beams, vocab, chunks, eos, dtype;
   // workspace
   float2* sums;               // [rows][chunks]: maximum, sum of exp(x - maximum)
   uint2* lists;               // [rows][chunks][beams]: key, token, highest first
@@ -253,142 +254,266 @@ __device__ __forceinline__ unsigned long long score_key64(double s) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
+__device__ __forceinline__ double key_score64(unsigned long long k) {
+  return __longlong_as_double((long long)(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+}
+
+// Largest error of a beam's log-sum-exp as the chunks give it.  Exponents in log2
+// units carry 2.3 x 2^-24 of their size (difference, product, the rounded
+// log2(e)), and the mean size under a chunk's softmax is at most the logarithm
+// of its 8,192 logits (the entropy is that mean and the sum's logarithm), 9.1 nats: 21 x 2^-24 of the
+// sum.  ex2.approx adds 4 x 2^-24 and 23 additions in a row 23 x 2^-24; the chunks are added in 64 bits.
+constexpr double kSumError = 1.0 / (1 << 18);
+
+// This thread's part of the sum of exp(logit - mx) over a row, in units of 2^-43 (x) and of 2^-86
+// (y, what those leave, of either sign): whole numbers, so that the sum does not depend on the
+// order and rows of the same logits have the same one.  At most 2^20 terms of at most
+// 2^43: modulo 2^64 they fit.  A term is rounded to either unit by an addition that leaves it in the last bits of
+// the sum; conversions to integers cost as much as the exponential.
+__device__ __noinline__ ulonglong2 exact_sum(const uint8_t* base, int dtype, int vocab, float mx) {
+  constexpr double kOne = 0x1p9, kTwo = 1.5 * 0x1p-34;   // last bits 2^-43 and 2^-86
+  ulonglong2 sum = {0ull, 0ull};
+  auto add = [&](float x) {
+    const double t = exp((double)x - (double)mx);
+    const double a = __dadd_rn(t, kOne), b = __dadd_rn(__dsub_rn(t, __dsub_rn(a, kOne)), kTwo);
+    sum.x += __double_as_longlong(a) - __double_as_longlong(kOne);
+    sum.y += __double_as_longlong(b) - __double_as_longlong(kTwo);
+  };
+  auto widen = [&](uint32_t h) {
+    return dtype == MK_DTYPE_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+  };
+  const int size = dtype == MK_DTYPE_F32 ? 4 : 2, of16 = 16 / size;
+  const int whole = (reinterpret_cast<uintptr_t>(base) & 15u) ? 0 : vocab / of16;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < whole; i += blockDim.x) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(base) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (size == 4) {
+        add(__uint_as_float(w[e]));
+      } else {
+        add(widen(w[e] & 0xFFFFu));
+        add(widen(w[e] >> 16));
+      }
+    }
+  }
+  for (int i = whole * of16 + threadIdx.x; i < vocab; i += blockDim.x)
+    add(size == 4 ? __ldcg(reinterpret_cast<const float*>(base) + i)
+                  : widen(__ldcg(reinterpret_cast<const uint16_t*>(base) + i)));
+  return sum;
+}
+
 __device__ __forceinline__ bool finished_of(const SelectArgs& a, size_t row) {
   return a.finished && __ldcg(a.finished + row);
 }
 
+// Warps of a join beside those of its beams help with sums that are taken again.
+__host__ __device__ constexpr int join_threads(int beams) { return beams == 1 ? 32 : beams > 4 ? beams * 32 : 128; }
+
 // One CTA a search, one warp a beam.  HEADS: chunk heads of a lane.  WT: most beams.
+// Where candidates of two beams are closer than the error of their sums (neighbours
+// 0.1 apart are that close once in 13,000 times), those beams' sums are taken
+// again in 64 bits and the choice is made again.  It costs 0.2 to 0.8 us where nothing is
+// close (8 beams of 128,256 fp32 10.1 -> 10.5 us) and 90 to 130 us for each
+// such beam of that size; beams that all hold the same logits 706 us.
 template <int HEADS, int WT>
-__global__ void __launch_bounds__(WT * 32) beam_join_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(join_threads(WT)) beam_join_kernel(const SelectArgs a) {
   constexpr int kOwn = WT * WT < 32 ? 1 : WT * WT / 32;   // candidates of a lane
   __shared__ __align__(16) uint2 few[WT][HEADS * 32 > WT * WT ? HEADS * 32 : WT * WT];   // heads, then candidates
   __shared__ int chosen[WT][WT];
   __shared__ uint32_t bound[WT];
   __shared__ double cand_score[WT][WT];
+  __shared__ float cand_logit[WT][WT];
   __shared__ int32_t cand_token[WT][WT];
+  __shared__ float highest[WT];
+  __shared__ unsigned long long total[2];
+  __shared__ uint32_t unsure;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5, W = a.beams;
   const size_t row = (size_t)blockIdx.x * W + beam;
-  const float2* sums = a.sums + row * a.chunks;
-  const uint2* lists = a.lists + row * a.chunks * W;
-  // all in flight at once (a finished beam's are not written: not used)
-  const double cum = __ldcg(a.cum + row);
-  const bool finished = finished_of(a, row);
-  float2 sum_of[HEADS];
-  uint2 head[HEADS];
+  // all in flight at once (a finished beam's sums and lists are not written: not used)
+  const double cum = beam < W ? __ldcg(a.cum + row) : 0.0;
+  const bool ended = beam == 0 && lane < W && finished_of(a, (size_t)blockIdx.x * W + lane);
+  if (beam < W) {
+    const float2* sums = a.sums + row * a.chunks;
+    const uint2* lists = a.lists + row * a.chunks * W;
+    const bool finished = finished_of(a, row);
+    float2 sum_of[HEADS];
+    uint2 head[HEADS];
 #pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int c = i * 32 + lane;
-    sum_of[i] = c < a.chunks ? __ldcg(sums + c) : make_float2(-INFINITY, 0.f);
-    head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
-  }
-  for (int j = lane; j < W; j += 32) {   // no candidates so far
-    cand_score[beam][j] = -INFINITY;
-    chosen[beam][j] = -1;
-  }
-  if (lane == 0) bound[beam] = 0u;
-  if (finished) {
-    __syncwarp();
-    if (lane == 0) {
-      cand_score[beam][0] = cum;
-      cand_token[beam][0] = a.eos;
+    for (int i = 0; i < HEADS; ++i) {
+      const int c = i * 32 + lane;
+      sum_of[i] = c < a.chunks ? __ldcg(sums + c) : make_float2(-INFINITY, 0.f);
+      head[i] = c < a.chunks ? __ldcg(lists + (size_t)c * W) : make_uint2(0u, 0u);
     }
-  } else {
+    for (int j = lane; j < W; j += 32) {   // no candidates so far
+      cand_score[beam][j] = -INFINITY;
+      chosen[beam][j] = -1;
+    }
+    if (lane == 0) bound[beam] = 0u;
+    if (finished) {
+      __syncwarp();
+      if (lane == 0) {
+        cand_score[beam][0] = cum;
+        cand_token[beam][0] = a.eos;
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) few[beam][i * 32 + lane] = head[i];
-    __syncwarp();
-    // the W chunks with the highest heads, by counting the heads before each (a
-    // head's token tells ties apart); the last of them bounds the beam's W best
-    const uint4* two = reinterpret_cast<const uint4*>(few[beam]);
-    int rank[HEADS];
+      for (int i = 0; i < HEADS; ++i) few[beam][i * 32 + lane] = head[i];
+      __syncwarp();
+      // the W chunks with the highest heads, by counting the heads before each (a
+      // head's token tells ties apart); the last of them bounds the beam's W best
+      const uint4* two = reinterpret_cast<const uint4*>(few[beam]);
+      int rank[HEADS];
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) rank[i] = 0;
-    const int pairs = (min(a.chunks, HEADS * 32) + 1) / 2;
+      for (int i = 0; i < HEADS; ++i) rank[i] = 0;
+      const int pairs = (min(a.chunks, HEADS * 32) + 1) / 2;
 #pragma unroll 4
-    for (int j = 0; j < pairs; ++j) {
-      const uint4 o = two[j];
+      for (int j = 0; j < pairs; ++j) {
+        const uint4 o = two[j];
 #pragma unroll
-      for (int i = 0; i < HEADS; ++i) {
-        rank[i] += o.x > head[i].x || (o.x == head[i].x && o.y < head[i].y);
-        rank[i] += o.z > head[i].x || (o.z == head[i].x && o.w < head[i].y);
+        for (int i = 0; i < HEADS; ++i) {
+          rank[i] += o.x > head[i].x || (o.x == head[i].x && o.y < head[i].y);
+          rank[i] += o.z > head[i].x || (o.z == head[i].x && o.w < head[i].y);
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i)
-      if (head[i].x && rank[i] < W) {
-        chosen[beam][rank[i]] = i * 32 + lane;
-        if (rank[i] == W - 1) bound[beam] = head[i].x;
+      for (int i = 0; i < HEADS; ++i)
+        if (head[i].x && rank[i] < W) {
+          chosen[beam][rank[i]] = i * 32 + lane;
+          if (rank[i] == W - 1) bound[beam] = head[i].x;
+        }
+      __syncwarp();
+      // their lists, in flight during the log-sum-exp over all chunks
+      uint2 c[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int e = i * 32 + lane, from = e / W;
+        const int chunk = e < W * W ? chosen[beam][from] : -1;
+        c[i] = chunk >= 0 ? __ldcg(lists + (size_t)chunk * W + (e - from * W)) : make_uint2(0u, 0u);
       }
-    __syncwarp();
-    // their lists, in flight during the log-sum-exp over all chunks
-    uint2 c[kOwn];
+      float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const int e = i * 32 + lane, from = e / W;
-      const int chunk = e < W * W ? chosen[beam][from] : -1;
-      c[i] = chunk >= 0 ? __ldcg(lists + (size_t)chunk * W + (e - from * W)) : make_uint2(0u, 0u);
-    }
-    float mx = -INFINITY;
+      for (int i = 0; i < HEADS; ++i) mx = fmaxf(mx, sum_of[i].x);
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) mx = fmaxf(mx, sum_of[i].x);
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+      double sum = 0.0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    double sum = 0.0;
+      for (int i = 0; i < HEADS; ++i)
+        // a chunk without a candidate has maximum -inf and adds its sum: 0, or a NaN
+        sum += sum_of[i].x > -INFINITY ? (double)sum_of[i].y * exp((double)sum_of[i].x - (double)mx) : (double)sum_of[i].y;
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i)
-      // a chunk without a candidate has maximum -inf and adds its sum: 0, or a NaN
-      sum += sum_of[i].x > -INFINITY ? (double)sum_of[i].y * exp((double)sum_of[i].x - (double)mx) : (double)sum_of[i].y;
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      const double lse = (double)mx + log(sum);
+      if (lane == 0) highest[beam] = mx;
+      // the beam's W best: of the few from the bound on, again by counting
+      const uint32_t least = max(bound[beam], 1u);
+      int n = 0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const double lse = (double)mx + log(sum);
-    // the beam's W best: of the few from the bound on, again by counting
-    const uint32_t least = max(bound[beam], 1u);
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const uint32_t in = __ballot_sync(0xFFFFFFFFu, c[i].x >= least);
-      if (c[i].x >= least) few[beam][n + __popc(in & ((1u << lane) - 1u))] = c[i];
-      n += __popc(in);
-    }
-    __syncwarp();
-    for (int e = lane; e < n; e += 32) {
-      const uint2 me = few[beam][e];
-      int before = 0;
+      for (int i = 0; i < kOwn; ++i) {
+        const uint32_t in = __ballot_sync(0xFFFFFFFFu, c[i].x >= least);
+        if (c[i].x >= least) few[beam][n + __popc(in & ((1u << lane) - 1u))] = c[i];
+        n += __popc(in);
+      }
+      __syncwarp();
+      for (int e = lane; e < n; e += 32) {
+        const uint2 me = few[beam][e];
+        int before = 0;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const uint2 o = few[beam][j];
-        before += o.x > me.x || (o.x == me.x && o.y < me.y);
-      }
-      if (before < W) {
-        cand_score[beam][before] = cum + ((double)key_logit(me.x) - lse);
-        cand_token[beam][before] = (int32_t)me.y;
+        for (int j = 0; j < n; ++j) {
+          const uint2 o = few[beam][j];
+          before += o.x > me.x || (o.x == me.x && o.y < me.y);
+        }
+        if (before < W) {
+          cand_score[beam][before] = cum + ((double)key_logit(me.x) - lse);
+          cand_logit[beam][before] = key_logit(me.x);
+          cand_token[beam][before] = (int32_t)me.y;
+        }
       }
     }
   }
-  __syncthreads();
-  if (beam) return;
-  // W rounds over the beams' lists, a lane each: highest score, then lowest beam
-  int at = 0;
-  double mine = lane < W ? cand_score[lane][0] : -INFINITY;
-  for (int j = 0; j < W; ++j) {
-    const unsigned long long key = score_key64(mine);
-    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32));
-    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
-    const bool real = (hi | lo) != 0u;
-    const int who = __ffs(__ballot_sync(0xFFFFFFFFu, key == ((unsigned long long)hi << 32 | lo))) - 1;
-    // fewer candidates than beams: a dead one, which keeps its own state
-    if (real ? lane == who : lane == j) {
-      const size_t to = (size_t)blockIdx.x * W + j;
-      const int token = real ? cand_token[lane][at] : max(a.eos, 0);
-      a.tokens[to] = token;
-      a.parents[to] = lane;
-      a.scores[to] = real ? (float)mine : -INFINITY;
-      if (a.done) a.done[to] = finished_of(a, (size_t)blockIdx.x * W + lane) || (a.eos >= 0 && token == a.eos);
-      if (real) {
-        ++at;
-        mine = at < W ? cand_score[lane][at] : -INFINITY;
+  // beams whose scores carry no error of a sum (the first warp's)
+  uint32_t exact = __ballot_sync(0xFFFFFFFFu, ended);
+#pragma unroll 1
+  for (;;) {
+    __syncthreads();
+    if (beam == 0) {
+      // W rounds over the beams' lists, a lane each: highest score, then lowest beam
+      int at = 0;
+      double mine = lane < W ? cand_score[lane][0] : -INFINITY;
+      unsigned long long chosen_key = 0ull;   // lane j: the j-th choice, 0 a dead one
+      int chosen_beam = 0;
+      for (int j = 0; j < W; ++j) {
+        const unsigned long long key = score_key64(mine);
+        const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32));
+        const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
+        const unsigned long long best = (unsigned long long)hi << 32 | lo;
+        const bool real = best != 0ull;
+        const int who = __ffs(__ballot_sync(0xFFFFFFFFu, key == best)) - 1;
+        if (lane == j) {
+          chosen_key = best;
+          chosen_beam = who;
+        }
+        // fewer candidates than beams: a dead one, which keeps its own state
+        if (real ? lane == who : lane == j) {
+          const size_t to = (size_t)blockIdx.x * W + j;
+          const int token = real ? cand_token[lane][at] : max(a.eos, 0);
+          a.tokens[to] = token;
+          a.parents[to] = lane;
+          a.scores[to] = real ? (float)mine : -INFINITY;
+          if (a.done) a.done[to] = ended || (a.eos >= 0 && token == a.eos);
+          if (real) {
+            ++at;
+            mine = at < W ? cand_score[lane][at] : -INFINITY;
+          }
+        }
       }
+      // Beams that a choice could have gone the other way for: of neighbours in the order, and
+      // of the last choice and each beam's next candidate.  (What is close to a choice
+      // further off is close to all in between.)
+      uint32_t close = 0u;
+      if (W > 1) {
+        auto close_to = [&](unsigned long long key, int b, double below, int b2) -> uint32_t {
+          const bool e = exact >> b & 1u, e2 = exact >> b2 & 1u;
+          const double from = key_score64(key) - (e || e2 ? kSumError : 2 * kSumError);
+          return key && b != b2 && !(e && e2) && below >= from ? 1u << b | 1u << b2 : 0u;
+        };
+        const unsigned long long next_key = __shfl_down_sync(0xFFFFFFFFu, chosen_key, 1),
+                                 last_key = __shfl_sync(0xFFFFFFFFu, chosen_key, W - 1);
+        const int next_beam = __shfl_down_sync(0xFFFFFFFFu, chosen_beam, 1),
+                  last_beam = __shfl_sync(0xFFFFFFFFu, chosen_beam, W - 1);
+        if (lane < W) close = close_to(last_key, last_beam, mine, lane);
+        if (lane + 1 < W && next_key) close |= close_to(chosen_key, chosen_beam, key_score64(next_key), next_beam);
+        close = __reduce_or_sync(0xFFFFFFFFu, close) & ~exact;
+      }
+      exact |= close;
+      if (lane == 0) unsure = close;
+    }
+    __syncthreads();
+    uint32_t left = unsure;   // the same for all, and new beams each time round
+    if (left == 0u) return;
+    for (; left; left &= left - 1u) {
+      const int b = __ffs(left) - 1;
+      if (threadIdx.x < 2) total[threadIdx.x] = 0ull;
+      __syncthreads();
+      ulonglong2 sum = exact_sum(static_cast<const uint8_t*>(a.logits) + ((size_t)blockIdx.x * W + b) * a.stride,
+                                a.dtype, a.vocab, highest[b]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, o);
+        sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, o);
+      }
+      if (lane == 0) {
+        atomicAdd(&total[0], sum.x);
+        atomicAdd(&total[1], sum.y);
+      }
+      __syncthreads();
+      if (beam == b && lane < W && cand_score[b][lane] > -INFINITY)
+        cand_score[b][lane] = cum + ((double)cand_logit[b][lane] -
+                                     ((double)highest[b] + log(((double)total[0] + (double)(long long)total[1] * 0x1p-43) * 0x1p-43)));
+      __syncthreads();
     }
   }
 }
@@ -522,7 +647,7 @@ extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_s
   a.logits = logits_dev; a.stride = (size_t)row_stride * esz;
   a.cum = cum_dev; a.finished = finished_dev;
   a.tokens = tokens_dev; a.parents = parents_dev; a.scores = scores_dev; a.done = finished_out_dev;
-  a.beams = beams; a.vocab = vocab; a.eos = eos;
+  a.beams = beams; a.vocab = vocab; a.eos = eos; a.dtype = dtype;
   a.chunks = (vocab + chunk_of(dtype) - 1) / chunk_of(dtype);
   const bool wide = ((reinterpret_cast<uintptr_t>(logits_dev) | a.stride) & 15u) == 0;
   const size_t rows = (size_t)n_batch * beams;
@@ -536,7 +661,7 @@ extern "C" int mk_beam_select(const void* logits_dev, int dtype, long long row_s
   auto join = beams <= 4 ? (a.chunks <= 64 ? beam_join_kernel<2, 4> : beam_join_kernel<8, 4>)
               : beams <= 8 ? (a.chunks <= 64 ? beam_join_kernel<2, 8> : beam_join_kernel<8, 8>)
                            : (a.chunks <= 64 ? beam_join_kernel<2, 16> : beam_join_kernel<8, 16>);
-  if (e == cudaSuccess) e = pdl_launch(join, dim3(n_batch), dim3(32 * beams), 0, st, a);
+  if (e == cudaSuccess) e = pdl_launch(join, dim3(n_batch), dim3(join_threads(beams)), 0, st, a);
   return e == cudaSuccess ? MK_OK : fail(MK_ERR_CUDA, who, cudaGetErrorString(e));
 }
 

@@ -1,5 +1,7 @@
 """Beam search's selection and reordering on the GPU against plain references
 in 64 bits, and a whole search on the decoder."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -135,6 +137,110 @@ def test_select_masked_tail_and_extreme_logits(cuda_ok):
     x[:, 13000:] = -float("inf")
     x[0, 0], x[1, 12999] = 3.0e38, -3.0e38
     _check(x.cuda(), torch.tensor([[0.0, -1.0, -2.0, -1000.0]]).cuda())
+
+
+def _exact(logits, cum):
+    """tokens and parents of the highest scores, each row's sum of exponentials
+    rounded once (math.fsum: rows of the same logits in another order have the
+    same), and the smallest distance of two scores of different beams that
+    are not equal, among the W + 1 first."""
+    n, W, V = logits.shape
+    tok, par, gap = [], [], np.inf
+    for b in range(n):
+        found = []
+        for w in range(W):
+            x = logits[b, w]
+            lse = x.max() + math.log(math.fsum(np.exp(x - x.max())))
+            order = np.argsort(-x, kind="stable")[:W + 1]
+            found += [(-(cum[b, w] + (x[v] - lse)), w, i, v) for i, v in enumerate(order)]
+        found = sorted(found)[:W + 1]
+        for f, g in zip(found, found[1:]):
+            if f[1] != g[1] and f[0] != g[0]:
+                gap = min(gap, g[0] - f[0])
+        tok.append([f[3] for f in found[:W]])
+        par.append([f[1] for f in found[:W]])
+    return np.array(tok), np.array(par), gap
+
+
+def _check_exact(logits, cum):
+    tok, par, sc, _ = _run(logits, cum)
+    n, W = cum.shape
+    want = _exact(logits.double().cpu().numpy().reshape(n, W, -1), cum.double().cpu().numpy())
+    assert want[2] > 1e-12          # far above what 64 bits lose
+    assert np.array_equal(par.cpu().numpy(), want[1])
+    assert np.array_equal(tok.cpu().numpy(), want[0])
+    assert (sc[:, 1:] <= sc[:, :-1]).all()
+
+
+def _shuffled(n, W, V, dtype, seed):
+    """Rows of a search: one row's logits, each time in another order."""
+    g = torch.Generator().manual_seed(seed)
+    one = (3 * torch.randn(n, 1, V, generator=g)).to(dtype).expand(n, W, V)
+    at = torch.rand(n, W, V, generator=g).argsort(-1)
+    return one.gather(2, at).reshape(n * W, V).contiguous()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,W,V", [(6, 2, 9001), (4, 3, 40000), (3, 8, 30011), (1, 4, 151936), (2, 16, 5000)])
+def test_select_equal_sums_of_shuffled_rows_go_to_the_lowest_beam(cuda_ok, dtype, n, W, V):
+    """Equal sums and the same logits in another order: every score is a tie of
+    all beams, whatever order a kernel adds in."""
+    _check_exact(_shuffled(n, W, V, TYPES[dtype], V + W).cuda(), torch.full((n, W), -1.25, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,W,V,step", [(8, 2, 9001, 1), (4, 4, 60000, 2), (2, 8, 30011, 3), (3, 16, 4097, 1), (1, 2, 151936, 1)])
+def test_select_orders_beams_a_rounding_apart(cuda_ok, dtype, n, W, V, step):
+    """Sums `step` fp32 numbers apart (6e-8 each), higher ones in random places."""
+    x = _shuffled(n, W, V, TYPES[dtype], V)
+    cum = np.full((n, W), np.float32(-0.75)).view(np.int32)
+    rng = np.random.default_rng(W)
+    cum = cum + step * np.stack([rng.permutation(W) for _ in range(n)]).astype(np.int32)
+    _check_exact(x.cuda(), torch.from_numpy(cum.astype(np.int32).view(np.float32)).cuda())
+
+
+def test_select_orders_beams_whose_sums_differ_in_the_tail(cuda_ok):
+    """Same highest logits, sums of exponentials 3e-8 to 4e-7 apart by one logit
+    far down; a finished beam whose sum lies in between."""
+    n, W, V = 4, 4, 50000
+    x = _shuffled(n, W, V, torch.float32, 5).view(n, W, V)
+    rng = np.random.default_rng(5)
+    for b in range(n):
+        for w, k in enumerate(rng.permutation(W)):
+            low = int(x[b, w].argmin())
+            lse = float(torch.logsumexp(x[b, w].double(), 0))
+            x[b, w, low] = lse + math.log(1e-7 * (k + 0.3))
+    cum = torch.full((n, W), -2.0)
+    _check_exact(x.reshape(n * W, V).cuda(), cum.cuda())
+    # beam 2 has finished, its sum the fp32 number next to the best score of beam 0
+    finished = torch.zeros(n, W, dtype=torch.bool)
+    finished[:, 2] = True
+    for b in range(n):
+        best = float(x[b, 0].max().double() - torch.logsumexp(x[b, 0].double(), 0)) - 2.0
+        cum[b, 2] = best
+    flat = x.reshape(n * W, V)
+    tok, par, sc, _ = _run(flat.cuda(), cum.cuda(), finished.cuda(), 9)
+    want = _reference(flat.double().numpy().reshape(n, W, V), cum.double().numpy(), finished.numpy(), 9)
+    assert np.array_equal(par.cpu().numpy(), want[1]) and np.array_equal(tok.cpu().numpy(), want[0])
+
+
+def test_select_close_beams_replayed_and_repeated(cuda_ok):
+    """The same bits from a graph and from every call, also where beams are close."""
+    x = _shuffled(4, 4, 20000, torch.float16, 3).cuda()
+    cum = torch.full((4, 4), -3.0, device="cuda")
+    first = _run(x, cum)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, _run(x, cum)))
+    tok = torch.zeros(4, 4, dtype=torch.int32, device="cuda")
+    par, sc = torch.zeros_like(tok), torch.zeros(4, 4, device="cuda")
+    ws = torch.empty(binding.beam_select_workspace_bytes(4, 4, 20000), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.beam_select(x, cum, tok, par, sc, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first[:3], (tok, par, sc)))
 
 
 def test_select_without_finished_flags_out(cuda_ok):
@@ -380,3 +486,4 @@ def test_beam_search_matches_a_search_by_prefills(cuda_ok, page, beams, eos):
         assert [tuple(r) for r in got.cpu().tolist()] == [h[0] for h in hyps]
     dec.close()
     host.close()
+
