@@ -406,12 +406,18 @@ class Decoder:
         log-probabilities [beams] fp32).  Sequences that reached ``eos`` (>= 0)
         go on with it.  Uses slots 0..beams-1; after the prefill, steps,
         selection and the caches' reordering are enqueued without a host round
-        trip, all on the decoder's stream, whose work the results are."""
+        trip on the decoder's stream, which waits for the caller's current
+        stream first; that waits for the results."""
         if not 1 <= beams <= self.max_batch:
             raise ValueError("beams is 1 to max_batch")
         n, V, dev = prompt_dev.numel(), self.model.vocab, prompt_dev.device
         if n_steps < 1 or n + n_steps - 1 > self.max_seq:
             raise ValueError("prompt and steps fit max_seq")
+        caller = torch.cuda.current_stream(dev)
+        apart = caller != self.stream
+        if apart:      # the prompt may still be on its way
+            self.stream.wait_stream(caller)
+            prompt_dev.record_stream(self.stream)
         with torch.cuda.device(dev), torch.cuda.stream(self.stream):
             logits = torch.empty(beams, V, device=dev)
             cum, done = torch.full((2, 1, beams), float("-inf"), device=dev), None
@@ -436,7 +442,12 @@ class Decoder:
                 seq[:, s] = tok.view(-1)
                 if s + 1 < n_steps:
                     self.decode_slots(tok.view(-1), [n + s] * beams, list(range(beams)), logits)
-        return seq, cum[n_steps % 2].view(-1)
+        sums = cum[n_steps % 2].view(-1)
+        if apart:
+            caller.wait_stream(self.stream)
+            for t in (seq, sums):
+                t.record_stream(caller)
+        return seq, sums
 
     def kv_free_pages(self) -> int:
         n = lib().mk_kv_free_pages(self.h)

@@ -487,3 +487,27 @@ def test_beam_search_matches_a_search_by_prefills(cuda_ok, page, beams, eos):
     dec.close()
     host.close()
 
+
+def test_beam_search_waits_for_its_prompt_and_is_waited_for(cuda_ok):
+    """A decoder on a stream of its own, the prompt still being written on the
+    caller's, the results read there at once: no wait on the host."""
+    model = synth.TINY
+    w = {k: v.cuda() for k, v in synth.make_model(model, 3).items()}
+    prompt = synth.make_prompt(12, model.vocab).cuda()
+    torch.cuda.synchronize()
+    dec = binding.Decoder(model, w, 64, max_batch=4, stream=torch.cuda.Stream())
+    first = dec.beam_search(prompt, 4, 8)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in first]
+    late = torch.zeros_like(prompt)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        late.zero_()
+        torch.cuda._sleep(100_000_000)      # some 50 ms of the caller's stream
+        late.copy_(prompt)
+        got = dec.beam_search(late, 4, 8)
+        seen = [t.clone() for t in got]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(seen, want))
+    assert dec.status() == 0
+    dec.close()
