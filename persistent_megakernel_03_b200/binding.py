@@ -11,8 +11,6 @@ import ctypes as C
 import os
 from typing import Dict, List, Optional, Sequence
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 # MK_LIBRARY selects another build of the library (A/B comparisons of builds).
 LIB_PATH = os.environ.get("MK_LIBRARY") or os.path.join(HERE, "libmk.so")
@@ -300,6 +298,7 @@ class Decoder:
                  l2_prefetch: int = 0, prefill_steps: int = 0, batch_sequential: int = 0,
                  weight_format: int = 0, kv_page_tokens: int = 0, kv_pool_pages: int = 0,
                  prefill_per_operator: int = 0, prefill_attention: int = 0):
+        import torch
         L = lib()
         self.model = model
         self.max_seq = max_seq
@@ -393,6 +392,7 @@ class Decoder:
         """Positions [first, n_pos) of slot slots[b] (slot b without ``slots``)
         become those of slot slots[parents_dev[b]], in place (see
         mk_kv_reorder); ``parents_dev`` int32 CUDA, one entry per slot."""
+        import torch
         _tensor(parents_dev, torch.int32, "parents_dev")
         n = parents_dev.numel() if slots is None else len(slots)
         if n != parents_dev.numel():
@@ -408,6 +408,7 @@ class Decoder:
         selection and the caches' reordering are enqueued without a host round
         trip on the decoder's stream, which waits for the caller's current
         stream first; that waits for the results."""
+        import torch
         if not 1 <= beams <= self.max_batch:
             raise ValueError("beams is 1 to max_batch")
         n, V, dev = prompt_dev.numel(), self.model.vocab, prompt_dev.device
@@ -512,6 +513,7 @@ class Decoder:
 
 def read_probe(src_dev, sink_dev, stream=None):
     """Enqueues one read-only pass over ``src_dev`` (a contiguous CUDA tensor)."""
+    import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     nbytes = src_dev.numel() * src_dev.element_size()
     _check(lib().mk_read_probe(src_dev.data_ptr(), nbytes, sink_dev.data_ptr(), st.cuda_stream))
@@ -524,6 +526,7 @@ def attention_workspace_bytes(n_q_per_kv: int, head_dim: int, splits: int) -> in
 def attention_decode(q_dev, k_dev, v_dev, n_keys: int, splits: int, workspace_dev, out_dev,
                      stream=None):
     """Split-KV decode attention for one KV head (see mk_attention_decode)."""
+    import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     G, d = q_dev.shape
     _check(lib().mk_attention_decode(q_dev.data_ptr(), k_dev.data_ptr(), v_dev.data_ptr(),
@@ -535,6 +538,7 @@ def attention_decode_noalloc(q_dev, k_dev, v_dev, n_keys: int, splits: int, out_
                              stream=None):
     """mk_attention_decode with the library's static scratch instead of a
     caller workspace (see mk_attention_decode_noalloc)."""
+    import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     G, d = q_dev.shape
     _check(lib().mk_attention_decode_noalloc(q_dev.data_ptr(), k_dev.data_ptr(),
@@ -544,11 +548,13 @@ def attention_decode_noalloc(q_dev, k_dev, v_dev, n_keys: int, splits: int, out_
 
 # ------------------------------------- the state of a decode: 4-bit cache, beams
 
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_FLAGS = (torch.bool, torch.uint8)
+_DTYPES = {}   # MK_DTYPE_* by torch type, filled at the first use: this module loads without torch
 
 
 def _dtype(t) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"fp32, bf16 or fp16 expected, got {t.dtype}")
@@ -570,6 +576,7 @@ def _tensor(t, dtype, what, shape=None, device=None):
 def _on(device, stream, call, *args):
     """Runs ``call(*args, stream)`` with the tensors' device (index) current; the
     stream is ``stream``, or that device's current one."""
+    import torch
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if device == torch._C._cuda_getDevice():
         rc = call(*args, raw)
@@ -594,6 +601,7 @@ class Kv4Cache:
 
     def __init__(self, pool, lens, n_kv_heads: int, head_dim: int, page_tokens: int, table=None,
                  scores=None, k_log2: int = 0, v_log2: int = 0):
+        import torch
         page = lib().mk_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
         if page == 0:
             raise MkError(-9, "head_dim is 64 or 128, page_tokens a multiple of 32")
@@ -640,6 +648,7 @@ def kv4_append(cache: Kv4Cache, k, v, offsets, stream=None):
     """Packed new tokens k, v [tokens, n_kv_heads, head_dim] (token rows may be
     strided) into the cache; tokens offsets[s]..offsets[s+1] are the newest of
     sequence s, which cache.lens counts already (see mk_kv4_append)."""
+    import torch
     d = cache.device
     kp, ks, n = _rows(k, cache.n_kv_heads, cache.head_dim, "k", d)
     vp, vs, m = _rows(v, cache.n_kv_heads, cache.head_dim, "v", d)
@@ -694,6 +703,7 @@ def kv4_evict(src: Kv4Cache, dst: Kv4Cache, budget: int, keep_first: int, keep_l
     """The rows of src that a budget leaves -- its ends and the highest scores
     -- into dst, their slots into kept int32 [n_seq, n_kv_heads, budget] (see
     mk_kv4_evict)."""
+    import torch
     d = src.device
     if dst.device != d:
         raise ValueError(f"caches on devices {d} and {dst.device}")
@@ -704,6 +714,7 @@ def kv4_evict(src: Kv4Cache, dst: Kv4Cache, budget: int, keep_first: int, keep_l
 def kv4_reorder(cache: Kv4Cache, parents, first: int, n_keys: int, stream=None):
     """Reorders the sequences of each search in place: parents int32
     [n_seq / beams, beams] (see mk_kv4_reorder)."""
+    import torch
     if parents.dim() != 2 or parents.numel() != cache.n_seq:
         raise ValueError("parents is [searches, beams], one entry per sequence")
     d = cache.device
@@ -721,6 +732,7 @@ def beam_select(logits, cum, tokens, parents, scores, workspace, finished=None, 
     be strided), cum fp32 [n_batch, beams] -> tokens, parents int32, scores
     fp32 and finished_out (bool or uint8), all [n_batch, beams] (see
     mk_beam_select)."""
+    import torch
     shape, d = cum.shape, logits.get_device()
     if len(shape) != 2 or logits.dim() != 2 or logits.shape[0] != shape[0] * shape[1]:
         raise ValueError("cum is [n_batch, beams], logits [n_batch * beams, vocab]")
@@ -728,8 +740,9 @@ def beam_select(logits, cum, tokens, parents, scores, workspace, finished=None, 
     st = logits.stride()
     if d < 0 or (vocab > 1 and st[1] != 1):
         raise ValueError("logits: CUDA, contiguous rows")
-    if (finished is not None and finished.dtype not in _FLAGS) or \
-            (finished_out is not None and finished_out.dtype not in _FLAGS):
+    flags = (torch.bool, torch.uint8)
+    if (finished is not None and finished.dtype not in flags) or \
+            (finished_out is not None and finished_out.dtype not in flags):
         raise TypeError("finished flags are bool or uint8")
     _on(d, stream, lib().mk_beam_select, logits.data_ptr(), _dtype(logits), st[0] if rows > 1 else vocab,
         _tensor(cum, torch.float32, "cum", None, d),
@@ -745,6 +758,7 @@ def beam_reorder(state, parents, first: int, count: int, stream=None):
     any type) in place by parents int32 [n_batch, beams]; positions [first,
     first + count) of every segment move, the others stay (see
     mk_beam_reorder)."""
+    import torch
     base, d = _tensor(state, None, "state"), state.get_device()
     if state.dim() < 3 or parents.dim() != 2 or parents.numel() != state.shape[0]:
         raise ValueError("state is [n_batch * beams, segments, positions, ...], parents [n_batch, beams]")

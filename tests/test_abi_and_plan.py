@@ -6,6 +6,7 @@ import os
 import random
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -260,3 +261,28 @@ def test_qkv_packing_is_a_bijection_with_rope_pairs_adjacent(model):
     want = {(0, h, i) for h in range(nq) for i in range(d)} | \
            {(w, h, i) for w in (1, 2) for h in range(nkv) for i in range(d)}
     assert seen == want
+
+
+def test_host_functions_work_without_torch():
+    """The binding loads, and what needs no GPU runs, where torch is missing."""
+    code = """
+import sys
+from types import SimpleNamespace
+class Hidden:
+    def find_spec(self, name, path=None, target=None):
+        if name.split('.')[0] == 'torch':
+            raise ImportError(name)
+sys.meta_path.insert(0, Hidden())
+from persistent_megakernel_03_b200 import binding
+model = SimpleNamespace(n_layers=2, hidden=256, n_q_heads=4, n_kv_heads=2, head_dim=64, ffn=768, vocab=4096,
+                        rms_eps=1e-6, rope_theta=1e4, qkv_bias=False, tied_embeddings=False)
+assert binding.make_config(model, 64, 1).hidden == 256
+assert binding.qkv_row_source(model, 0) == (0, 0, 0)
+assert len(binding.Plan(model, 64, 148).tasks()) > 0
+assert binding.kv4_page_bytes(8, 128, 64) == 73728
+assert binding.beam_select_workspace_bytes(2, 4, 1000) == 320
+assert binding.attention_workspace_bytes(4, 128, 8) > 0
+assert 'torch' not in sys.modules
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
