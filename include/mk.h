@@ -467,7 +467,11 @@ int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, int dtype, in
  * (-1 behind the last).  src is only read, so a prompt's pages may be shared;
  * dst has pages and scores of its own (same heads, head_dim, n_seq and log2;
  * page_tokens may differ), and its lens become min(lens, budget) by the
- * caller.  1 <= budget <= dst's capacity; keep_first + keep_last <= budget. */
+ * caller.  1 <= budget <= dst's capacity; keep_first + keep_last <= budget.
+ * Every slot that lens counts has a page, in src and (the first budget of
+ * them) in dst; the caller sees to that.  Where one has none, the row is not
+ * copied: one kept from src, chosen by its score like any other, leaves its row
+ * of dst as it was, and lens would count that row as a key. */
 int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, int budget, int keep_first,
                  int keep_last, int32_t* kept_dev, void* stream);
 

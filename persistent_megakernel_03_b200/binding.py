@@ -701,8 +701,9 @@ def attention_kv4(cache: Kv4Cache, q, out, workspace, scale: Optional[float] = N
 def kv4_evict(src: Kv4Cache, dst: Kv4Cache, budget: int, keep_first: int, keep_last: int, kept,
               stream=None):
     """The rows of src that a budget leaves -- its ends and the highest scores
-    -- into dst, their slots into kept int32 [n_seq, n_kv_heads, budget] (see
-    mk_kv4_evict)."""
+    -- into dst, their slots into kept int32 [n_seq, n_kv_heads, budget].
+    Every slot that lens counts has a page, in src and, up to the budget, in
+    dst (see mk_kv4_evict)."""
     import torch
     d = src.device
     if dst.device != d:

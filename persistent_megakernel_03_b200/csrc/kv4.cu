@@ -565,6 +565,7 @@ constexpr int kMoveRows = 4;     // rows of a thread, their loads in flight toge
 
 // Copies the kept rows to their place in the other cache: 8 threads a row, 16
 // (d = 128) or 8 bytes of codes each, the scales beside the first of K and V.
+// A row that has no page, here or there, is skipped: callers give every slot that lens counts one.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads)
     kv4_move_kernel(Kv4 src, Kv4 dst, int budget, const int32_t* kept) {

@@ -818,6 +818,36 @@ def test_evict_with_missing_pages(cuda_ok):
     assert np.array_equal(dst.pool.cpu().numpy(), d.pool)
 
 
+@pytest.mark.parametrize("dim,page,to_page", [(64, 32, 64), (128, 64, 32)])
+def test_attention_after_an_eviction_sees_the_kept_rows_only(cuda_ok, dim, page, to_page):
+    """Every slot below lens has a page, as an eviction asks for; the
+    destination's pages held NaN before.  Longer, equal, shorter and empty
+    sequences; every KV head keeps slots of its own."""
+    lens, heads, group, budget = [300, 64, 65, 10, 0], 3, 2, 64
+    p = Plain(5, heads, dim, page, -(-300 // page), seed=4)
+    p.fill_random(lens)
+    scores = np.exp(2 * np.random.default_rng(1).normal(size=(5, heads, p.capacity))).astype(np.float32)
+    c = _cuda(p, lens, scores)
+    d = Plain(5, heads, dim, to_page, -(-budget // to_page), seed=5, fill=0xFF)
+    now = [min(n, budget) for n in lens]
+    dst = _cuda(d, now, np.full((5, heads, d.capacity), np.nan))
+    kept = torch.zeros(5, heads, budget, dtype=torch.int32, device="cuda")
+    binding.kv4_evict(c, dst, budget, 4, 16, kept)
+    q = torch.randn(5, 2, heads * group, dim, generator=torch.Generator().manual_seed(2)).cuda()
+    out = _attend(dst, q, True)
+    got = kept.cpu().numpy()
+    for s, n in enumerate(lens):
+        k, v = p.read(s, n)
+        at = got[s, :, :now[s]].T                                      # [slots][heads]
+        k, v = (np.take_along_axis(x, at[..., None], 0) for x in (k, v))
+        want, w, mass, reach = attend(q[s].double().cpu().numpy(), k, v, dim ** -0.5, group)
+        assert (np.abs(out[s].double().cpu().numpy() - want) <= _bound(want, mass, reach, q.dtype)).all()
+        before = np.take_along_axis(scores[s].astype(np.float64), at.T, 1)
+        t = 4 * 2.0 ** -18 * (reach.max() if reach.size else 0) + 2.0 ** -17
+        after = dst.scores[s, :, :now[s]].double().cpu().numpy()
+        assert (np.abs(after - before - w) <= w * t + (before + w) * 2.0 ** -22 + 1e-30).all()
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("captured", [False, True])
