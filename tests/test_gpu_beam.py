@@ -372,6 +372,33 @@ def test_kv4_reorder_moves_blocks_and_scores(cuda_ok, dim, page, paged, scores):
         assert np.array_equal(cache.scores.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("W,heads,dim,page,per,first,keys", [(4, 4, 128, 64, 40, 700, 2500), (8, 2, 64, 32, 130, 0, 4160)])
+def test_kv4_reorder_over_many_pages(cuda_ok, paged, W, heads, dim, page, per, first, keys):
+    n, blocks, size = 2, page // 32, 32 * (dim + dim // 8)
+    pages = n * W * per
+    g = torch.Generator("cuda").manual_seed(W)
+    pool = torch.randint(0, 256, (pages, heads * blocks * size), dtype=torch.uint8, device="cuda", generator=g)
+    table = (torch.randperm(pages, device="cuda", generator=g) if paged else torch.arange(pages, device="cuda")).view(n * W, per)
+    scores = torch.randn(n * W, heads, per * page, device="cuda", generator=g)
+    cache = binding.Kv4Cache(pool.clone(), torch.full((n * W,), keys, dtype=torch.int32, device="cuda"), heads, dim, page,
+                             table.int() if paged else None, scores.clone())
+    par = torch.randint(0, W, (n, W), device="cuda", generator=g).int()
+    binding.kv4_reorder(cache, par, first, keys)
+    rows = (par.long() + torch.arange(n, device="cuda").unsqueeze(1) * W).flatten()
+
+    def by_slot(x):   # [n * W][logical block][heads][bytes]
+        return x.view(pages, heads, blocks, size)[table].transpose(2, 3).flatten(1, 2)
+    b0, b1 = first // 32, -(-keys // 32)
+    old, got = by_slot(pool), by_slot(cache.pool)
+    want = old.clone()
+    want[:, b0:b1] = old[rows][:, b0:b1]
+    assert torch.equal(got, want)
+    want = scores.clone()
+    want[:, :, b0 * 32:b1 * 32] = scores[rows][:, :, b0 * 32:b1 * 32]
+    assert torch.equal(cache.scores, want)
+
+
 # ------------------------------------------------------------- the decoder
 
 def _decoder(model, w, max_seq, batch, page):

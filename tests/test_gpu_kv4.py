@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from persistent_megakernel_03_b200 import binding
-from kv4_util import GROUP, Plain, attend, values
+from kv4_util import GROUP, TINY, Plain, attend, values
 
 pytestmark = pytest.mark.gpu
 
@@ -405,6 +405,53 @@ def test_attention_of_scores_past_fp32(cuda_ok, dim, n, dtype, scale, k_log2):
     tol = np.abs(want) * torch.finfo(q.dtype).eps / 2 + mass * (PART[q.dtype] + 2.0 ** -18) + 2.0 ** -25
     assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
     assert (np.abs(c.scores[0, :, :n].double().cpu().numpy() - w) <= w * 2.0 ** -17 + 1e-30).all()
+
+
+def _reference64(c, q, scale):
+    """out, weights, and the bound's sums of attention over a cache's values as
+    read back, in 64 bits on the GPU, one sequence after another."""
+    n_seq, T, Hq, d = q.shape
+    group = Hq // c.n_kv_heads
+    n = int(c.lens.max())
+    k = torch.zeros(n_seq, n, c.n_kv_heads, d, device="cuda")
+    v = torch.zeros_like(k)
+    binding.kv4_read(c, k, v)
+    for s in range(n_seq):
+        m = int(c.lens[s])
+        kd = k[s, :m].double().transpose(0, 1).repeat_interleave(group, 0)          # [Hq][m][d]
+        vd = v[s, :m].double().transpose(0, 1).repeat_interleave(group, 0)
+        qd = q[s].double().transpose(0, 1)                                          # [Hq][T][d]
+        seen = torch.arange(m, device="cuda") < (m - T + 1 + torch.arange(T, device="cuda")).unsqueeze(-1)
+        x = (qd @ kd.transpose(1, 2) * scale).masked_fill(~seen, -float("inf"))
+        p = torch.softmax(x, -1).nan_to_num(0.0)
+        small = TINY * p.amax(-1, keepdim=True) * seen
+        reach = (qd.abs() @ kd.abs().transpose(1, 2) * scale).masked_fill(~seen, 0.0).amax(-1)
+        yield (s, m, (p @ vd).transpose(0, 1).cpu().numpy(), p.unflatten(0, (-1, group)).sum((1, 2)).cpu().numpy(),
+               ((p + small) @ vd.abs()).transpose(0, 1).cpu().numpy(), reach.transpose(0, 1).cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n_seq,lo,hi,heads,group,dim,q_len,page", [
+    (12, 6001, 8191, 8, 4, 128, 1, 128), (24, 3000, 4097, 4, 8, 64, 1, 64),    # long batches
+    (3, 500, 2100, 2, 8, 128, 6, 64), (2, 900, 1301, 4, 8, 128, 16, 32),       # 48 and 128 rows of a KV head
+    (2, 700, 2049, 1, 16, 128, 64, 64), (3, 1, 1500, 2, 5, 64, 33, 96),        # 1,024 rows; 165, with a short sequence
+])
+def test_attention_at_size(cuda_ok, dtype, n_seq, lo, hi, heads, group, dim, q_len, page):
+    rng = np.random.default_rng(hi)
+    lens = [lo, hi] + rng.integers(lo, hi + 1, n_seq - 2).tolist()
+    p = Plain(n_seq, heads, dim, page, -(-hi // page), seed=n_seq, k_log2=-1, v_log2=2)
+    p.fill_random(lens, size=1.5)
+    q = torch.randn(n_seq, q_len, heads * group, dim, generator=torch.Generator().manual_seed(hi)).to(TYPES[dtype]).cuda()
+    c = _cuda(p, lens, np.zeros((n_seq, heads, p.capacity)))
+    out = _attend(c, q, True)
+    for s, m, want, w, mass, reach in _reference64(c, q, dim ** -0.5):
+        err, tol = np.abs(out[s].double().cpu().numpy() - want), _bound(want, mass, reach, q.dtype)
+        assert (err <= tol).all(), (s, (err / tol).max())
+        # a weight as in _check; up to 1,024 of them added one after another in fp32
+        t = 4 * 2.0 ** -18 * reach.max() + 2.0 ** -17 + q_len * group * 2.0 ** -24
+        got = c.scores[s].double().cpu().numpy()
+        assert (np.abs(got[:, :m] - w) <= w * t + 1e-30).all(), s
+        assert (got[:, m:] == 0).all()
 
 
 def test_attention_small_weights_add_up(cuda_ok):
