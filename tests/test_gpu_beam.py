@@ -538,3 +538,49 @@ def test_beam_search_waits_for_its_prompt_and_is_waited_for(cuda_ok):
         assert all(torch.equal(a, b) for a, b in zip(seen, want))
     assert dec.status() == 0
     dec.close()
+
+
+@pytest.mark.parametrize("mseed,pseed,beams,page,eos", [
+    (3, 3, 3, 0, False), (3, 3, 4, 64, False), (4, 1, 4, 0, False), (3, 4, 3, 64, False), (5, 2, 4, 0, False),
+    (3, 5, 3, 0, True), (4, 2, 3, 64, True), (3, 2, 4, 0, True)])
+def test_beam_search_matches_a_search_that_replays_every_hypothesis(cuda_ok, mseed, pseed, beams, page, eos):
+    """Against a search on the host whose hypotheses are decoded from the prompt
+    again at every step, each in the slot where the search holds it: the same
+    kernels on the same tokens, so the logits are the same and only the
+    selection's sums differ, 2^-18 and a rounding to fp32 a step.  The prompts
+    are such that all choices lie further apart; then tokens, order and sums follow."""
+    model, n, steps = synth.TINY, 12, 6
+    w = {k: v.cuda() for k, v in synth.make_model(model, mseed).items()}
+    w["lm_head"] = (w["lm_head"].float() * 20).to(torch.bfloat16)      # logits that tell tokens apart
+    prompt = synth.make_prompt(n, model.vocab, pseed).cuda()
+    dec, host = (_decoder(model, w, 64, beams, page) for _ in range(2))
+    end = int(dec.beam_search(prompt, beams, 2)[0][1, 0]) if eos else -1
+    got, sums = dec.beam_search(prompt, beams, steps, eos=end)
+    logits = torch.empty(beams, model.vocab, device="cuda")
+    slots = list(range(beams))
+    hyps, close = [((), 0.0)], np.inf
+    for s in range(steps):
+        for b in slots:
+            host.prefill_slots(prompt, [0, n], [b], logits[b:b + 1])
+        for i in range(s):
+            toks = torch.tensor([h[0][i] for h in hyps], dtype=torch.int32, device="cuda")
+            host.decode_slots(toks, [n + i] * beams, slots, logits)
+        lp = torch.log_softmax(logits.double(), -1).cpu().numpy()
+        found = []
+        for b, (toks, total) in enumerate(hyps):
+            if end in toks:
+                found.append((toks + (end,), total))
+            else:
+                found += [(toks + (int(v),), total + lp[b, v]) for v in np.argsort(-lp[b], kind="stable")[:beams + 1]]
+        found.sort(key=lambda f: -f[1])
+        close = min([close] + [a[1] - b[1] for a, b in zip(found[:beams], found[1:])])
+        hyps = found[:beams]
+    torch.cuda.synchronize()
+    bar = steps * (2.0 ** -18 + 2.0 ** -24 * abs(hyps[-1][1]))
+    assert close > 2 * bar, close
+    assert [tuple(r) for r in got.cpu().tolist()] == [h[0] for h in hyps]
+    assert np.abs(sums.cpu().numpy() - np.array([h[1] for h in hyps])).max() <= bar
+    assert not eos or any(end in h[0] for h in hyps)
+    assert dec.status() == 0 and host.status() == 0
+    dec.close()
+    host.close()
