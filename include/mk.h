@@ -441,17 +441,19 @@ int mk_kv4_read(const mk_kv4_cache* cache, int dtype, int n, void* k_out_dev, vo
  * query heads: token i of sequence s sees slots j < lens[s] - q_len + i + 1
  * (its own key included), out = softmax(scale * q k^T) v.  q_dev: `dtype`
  * [n_seq * q_len][n_q_heads][head_dim], tokens q_stride elements apart, 16-byte
- * aligned, finite (a row that is not gets NaN, the others stay right); query head h uses KV head h / (n_q_heads / n_kv_heads); q_len *
- * n_q_heads / n_kv_heads <= 1024; 1e-18 <= scale <= 1e18.  out_dev: the same type,
- * [n_seq][q_len][n_q_heads][head_dim], 16-byte aligned.  fp32 softmax and sums; queries and
- * probabilities enter the products with at least 22 bits (probabilities of a
- * bf16 call 11).  A token that sees nothing gets zeros (a sequence shorter than
- * q_len, an empty one); slots without a page are not seen, and what a masked
- * slot holds never matters.  accumulate != 0 adds, for every slot, the weights
- * of all tokens and query heads of its KV head to the cache's scores.
- * workspace_dev: mk_attention_kv4_workspace_bytes(...) bytes (0: an argument
- * is not supported), 16-byte aligned, any contents; with accumulate it grows
- * with n_seq * capacity * rows (the scores of every slot). */
+ * aligned, finite (a row that is not gets NaN, the others stay right); query
+ * head h uses KV head h / (n_q_heads / n_kv_heads); q_len * n_q_heads /
+ * n_kv_heads <= 1024; 1e-18 <= scale <= 1e18.  out_dev: the same type, [n_seq]
+ * [q_len][n_q_heads][head_dim], 16-byte aligned.  fp32 softmax and sums.  In
+ * the products a query element has at least 22 bits (bf16 and fp16 ones all of
+ * theirs) and a probability 22 (of a bf16 call 11), or, if small, an error of
+ * at most 2^-36 of its row's largest.  A token that sees nothing gets zeros (a
+ * sequence shorter than q_len, an empty one); slots without a page are not
+ * seen, and what a masked slot holds never matters.  accumulate != 0 adds, for
+ * every slot, the weights of all tokens and query heads of its KV head to the
+ * cache's scores.  workspace_dev: mk_attention_kv4_workspace_bytes(...) bytes
+ * (0: an argument is not supported), 16-byte aligned, any contents; with
+ * accumulate it grows with n_seq * capacity * rows (the scores of every slot). */
 size_t mk_attention_kv4_workspace_bytes(const mk_kv4_cache* cache, int q_len, int n_q_heads,
                                         int accumulate);
 int mk_attention_kv4(const mk_kv4_cache* cache, const void* q_dev, int dtype, int q_len,

@@ -139,7 +139,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // codes the reciprocal's product is corrected once by its exact remainder,
 // which leaves an error of 2^-47 before the rounding.  Comparing x with the
 // seven products midpoint * scale instead (exact as well) took 31 us where
-// this takes 14 (8 prompts, 8,300 tokens of 8 heads, d = 128): 21 integer
+// this takes 14 (8 prompts, 7,292 tokens of 8 heads, d = 128): 21 integer
 // instructions an element at half rate.  A NaN or infinity makes the scale NaN:
 // the whole group then reads back as NaN.
 __device__ __forceinline__ void quantize16(float (&x)[16], int neg_log2, uint2& codes, uint32_t& scale) {
@@ -312,7 +312,7 @@ constexpr int kReadThreads = 256;
 // of codes and writes whole rows.  A slot's bytes are found by two dependent
 // loads (length and page, then the row), so many warps an SM matter more than
 // work per thread: four slots a thread took the same time for a ragged batch of
-// 7,300 slots and 5 to 10 us more for one of 4,096.
+// 7,292 slots and 5 to 10 us more for one of 4,096.
 template <int D>
 __global__ void __launch_bounds__(kReadThreads)
     kv4_read_kernel(Kv4 c, int dtype, int n, uint8_t* k_out, uint8_t* v_out, bool whole, float k_mul, float v_mul) {

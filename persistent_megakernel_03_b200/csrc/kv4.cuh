@@ -67,9 +67,8 @@ __device__ __forceinline__ uint8_t* kv4_block(const Kv4& c, int page, int head, 
 }
 
 // Two e2m1 codes of a byte as fp16 values (low nibble in the low half), for
-// each byte of a word: cvt runs at 64 lanes a clock and SM, three times what
-// shifts and masks of the nibbles reach (42 against 25 pairs a clock with the
-// probe's own three instructions counted).
+// each byte of a word: cvt converts 42 pairs a clock and SM, shifts and masks of the
+// nibbles 25 (the probe's own three instructions counted in both).
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -86,12 +85,6 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
   return h;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // Checks an mk_kv4_cache; 0 or an MK_ERR_* code, with the reason in

@@ -26,11 +26,13 @@
 //    bytes, so that one cvt gives the mma's pair.
 //
 // Precision: code * scale is exact in fp16.  A query row is scaled by a power
-// of two to the top of fp16's range; bf16 and fp16 queries are then exact,
-// fp32 ones are the sum of two fp16 parts (22 bits).  Probabilities, biased so
-// that small ones stay normal, are one fp16 part for bf16 results (an error of
-// 2^-12 beside the result's 2^-9) and two for fp16 and fp32.  Scores, maxima,
-// sums and outputs are fp32.
+// of two that puts its largest element between 2^13 and 2^14.  bf16 elements are then
+// exact down to 2^-30 of the largest and fp16 ones to 2^-27; fp32 ones are the sum of two fp16
+// parts, 22 bits down to 2^-15 of the largest; anything smaller is off by at most 2^-38 of it
+// (half of fp16's last step).  Probabilities, 2^11 to 2^15 at the row's highest score, are
+// one fp16 part for bf16 results (an error of 2^-12 beside the result's 2^-9) and two for fp16
+// and fp32 (2^-22 down to 2^-13 of the highest); smaller ones are off by at most 2^-36 of it, and
+// vanish below that, while the sum still counts them.  Scores, maxima, sums and outputs are fp32.
 //
 // Work: the blocks of 32 keys of all (sequence, row tile, KV head) items stand
 // in one line, each item preceded by a few units for what starting it costs,
@@ -54,11 +56,11 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreadsA = kWarps * 32;
-constexpr int kStages = 2;        // blocks of a warp's ring: one loads while the other is used
+constexpr int kStages = 2;        // blocks of a warp's ring: one loads while the other is used (the code below counts on two)
 constexpr int kMaxCtas = 320;     // partials are laid out for this many CTAs
 constexpr int kMaxRows = 1024;    // query rows of a KV head: q_len * group
 // Probabilities are 2^(S - ref + kBias), S at most kSlack above the reference:
-// fp16 holds up to 2^15, and down to 2^-25 of the reference without loss.
+// fp16 holds up to 2^15, with all its bits down to 2^-25 of the reference.
 constexpr float kBias = 11.f;
 constexpr float kSlack = 4.f;
 
@@ -383,8 +385,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
     };
     uint32_t have = 0;   // bit i: the block i ahead of the current one has a page
     __syncwarp();        // the slots' last readers are done
-    // one block each first: copies are served in order, so a warp's second block
-    // would hold up the first one of the warps behind it
+    // One block now, the next when this one is in: copies are served in order, so a warp's
+    // second block would hold up the first one of the warps behind it.
     if (issue()) have |= 1u;
     cp_commit();
 
@@ -453,11 +455,6 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 2 : 1) kv4_attn_kernel(co
       see_all = min(see_all, lim[nt]);
     }
     see_all = __reduce_min_sync(0xFFFFFFFFu, see_all);
-#pragma unroll
-    for (int i = 1; i < kStages - 1; ++i) {
-      if (b0 + i < b1 && issue()) have |= 1u << i;
-      cp_commit();
-    }
 
     float o[NT][KS][4];
     float ref[NT][2], sum[NT][2];    // reference of the probabilities (log2 units), their sum
