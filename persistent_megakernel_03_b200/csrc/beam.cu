@@ -54,12 +54,6 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The lane whose (key, index) is first: highest key, then lowest index.
 __device__ __forceinline__ void warp_first(uint32_t key, uint32_t idx, uint32_t& k, uint32_t& i) {
   k = __reduce_max_sync(0xFFFFFFFFu, key);

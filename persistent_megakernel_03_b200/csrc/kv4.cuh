@@ -87,6 +87,13 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
   return h;
 }
 
+// 2^x: 2^-22 of the value, 0 for -inf.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Checks an mk_kv4_cache; 0 or an MK_ERR_* code, with the reason in
 // mk_last_error(NULL).  `who` names the entry point.
 int kv4_check(const mk_kv4_cache* c, const char* who);

@@ -3,11 +3,13 @@
 // waits there for it.  It saves the launch gap (1 to 2 us of a 5 us operator).
 //
 // Every kernel launched this way waits (pdl_wait) in every CTA before it
-// touches global memory that an earlier launch may write or read.  The wait
-// returns when the launch before is complete and its writes are visible; as
-// that launch waited for the one before it, all earlier work is complete too.
-// Such a kernel begins before its inputs are final, so it reads them with loads
-// that L2 answers (__ldcg, cp.async.cg), never through the read-only path.
+// touches global memory that an earlier launch may write or read; weights,
+// which none does, may be loaded before.  The wait returns when the launch
+// before is complete and its writes are visible; as that launch waited for the
+// one before it, all earlier work is complete too.  Such a kernel begins before
+// its inputs are final: the operators on a decode's state read them with loads
+// that L2 answers (__ldcg, cp.async.cg), never through the read-only path.  In
+// a normal launch both calls do nothing.
 #pragma once
 #include <cuda_runtime.h>
 

@@ -30,6 +30,7 @@
 #include "mk_internal.h"
 #include "prefill.h"
 #include "ptx.cuh"
+#include "pdl.cuh"
 #include "tc.cuh"
 
 namespace mk {
@@ -828,25 +829,6 @@ __global__ void b_ids_kernel(const unsigned long long* __restrict__ best, int n,
 
 // ------------------------------------------------------------------ host
 
-// Launch with programmatic stream serialization: the kernel may start while
-// the previous kernel of the stream runs; it calls pdl_wait() before reading
-// that kernel's results (the kernels above all do).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -887,7 +869,7 @@ std::string gemm(const uint16_t* W, int n_rows, int K, const uint16_t* xh, const
   const uint16_t* b = splits == 1 ? bias : nullptr;
   const size_t pst = (size_t)n_tok * ldy;
   if (pdl) {
-    const cudaError_t le = launch_pdl(gemm_wx_kernel<BN, STAGES>, grid, dim3(128),
+    const cudaError_t le = pdl_launch(gemm_wx_kernel<BN, STAGES>, grid, dim3(128),
                                       gemm_smem_bytes<BN, STAGES>(), st, mw, mh, mm, ml, n_rows, n_tok, K,
                                       Y, ldy, pst, b, err, tok_ss, K, norm_eps, (uint16_t*)nullptr, 0);
     if (le != cudaSuccess) return std::string("GEMM launch: ") + cudaGetErrorString(le);
@@ -919,11 +901,11 @@ std::string gemm_hl(const uint16_t* W, int n_rows, int K, const uint16_t* xhl, i
   const dim3 grid((n_rows + kGM - 1) / kGM, 1, splits);
   const cudaError_t le =
       two_per_sm
-          ? launch_pdl(gemm_wx_kernel<16, kDStagesPair, true>, grid, dim3(128),
+          ? pdl_launch(gemm_wx_kernel<16, kDStagesPair, true>, grid, dim3(128),
                        gemm_smem_bytes<16, kDStagesPair, true>(), st, mw, mh, mh, mh, n_rows, n_tok, K, Y,
                        ldy, (size_t)n_tok * ldy, (const uint16_t*)nullptr, err, tok_ss, K, norm_eps,
                        act_hl, n_rows / 2)
-          : launch_pdl(gemm_wx_kernel<16, kDStages, true>, grid, dim3(128),
+          : pdl_launch(gemm_wx_kernel<16, kDStages, true>, grid, dim3(128),
                        gemm_smem_bytes<16, kDStages, true>(), st, mw, mh, mh, mh, n_rows, n_tok, K, Y,
                        ldy, (size_t)n_tok * ldy, (const uint16_t*)nullptr, err, tok_ss, K, norm_eps,
                        act_hl, n_rows / 2);
@@ -1113,7 +1095,7 @@ std::string launch_batch_attn(dim3 grid, cudaStream_t st, const float* q, const 
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess
                ? "" : "batched attention shared memory attribute";
   }
-  const cudaError_t e = launch_pdl(k, grid, dim3(kBAWarps * 32), smem, st, q, bp, m, layer, S, num_sms,
+  const cudaError_t e = pdl_launch(k, grid, dim3(kBAWarps * 32), smem, st, q, bp, m, layer, S, num_sms,
                                    part, tickets, xh, xl);
   return e == cudaSuccess ? "" : std::string("batched attention launch: ") + cudaGetErrorString(e);
 }
@@ -1206,14 +1188,14 @@ std::string batch_enqueue(const ModelDev& m, const PrefillWeights& w, BatchScrat
     if (!(e = gemm_hl(w.qkv[l], qkvR, H, xhl, n, bs.y, ldy, bs.err, st, zq, ss_attn, m.rms_eps,
                       nullptr, true)).empty())
       return e;
-    CKL(launch_pdl(rope_kv_kernel, dim3(n, psl), dim3(256), 0, st, (const float*)bs.y, ldy, zq, pstride,
+    CKL(pdl_launch(rope_kv_kernel, dim3(n, psl), dim3(256), 0, st, (const float*)bs.y, ldy, zq, pstride,
                    bias, (const int32_t*)bp->slot, (const int32_t*)bp->pos, m, l, bs.q));
     if (!(e = batch_attn(dim3(bs.splits, m.n_kv, n), st, bs.q, bp, m, l, bs.splits, num_sms, bs.part, false,
                          bs.tickets, xhl, lo(qd))).empty())
       return e;
     if (!(e = gemm_hl(w.o[l], H, qd, xhl, n, bs.y, ldy, bs.err, st, zo, nullptr, 0.f, nullptr, true)).empty())
       return e;
-    CKL(launch_pdl(b_residual_norm_kernel, dim3(hsl, n), dim3(256), 0, st, bs.x, (const float*)bs.y, H,
+    CKL(pdl_launch(b_residual_norm_kernel, dim3(hsl, n), dim3(256), 0, st, bs.x, (const float*)bs.y, H,
                    ldy, zo, pstride, m.ffn_norm + (size_t)l * H, xhl, lo(H), ss_ffn));
     // SwiGLU output into a second buffer: the gate/up GEMM still reads xhl
     if (zg == 1) {  // in the GEMM's epilogue
@@ -1223,21 +1205,21 @@ std::string batch_enqueue(const ModelDev& m, const PrefillWeights& w, BatchScrat
     } else {
       if (!(e = gemm_hl(w.gu[l], 2 * F, H, xhl, n, bs.y, ldy, bs.err, st, zg, ss_ffn, m.rms_eps)).empty())
         return e;
-      CKL(launch_pdl(b_swiglu_kernel, dim3(fsl, n), dim3(256), 0, st, (const float*)bs.y, ldy, F, zg,
+      CKL(pdl_launch(b_swiglu_kernel, dim3(fsl, n), dim3(256), 0, st, (const float*)bs.y, ldy, F, zg,
                      pstride, bs.xh2, bs.xh2 + (size_t)8 * F));
     }
     if (!(e = gemm_hl(w.dn[l], H, F, bs.xh2, n, bs.y, ldy, bs.err, st, zd, nullptr, 0.f, nullptr, true)).empty())
       return e;
     // the residual add, then the next layer's attention norm (the final norm after the last)
     const uint16_t* next_norm = l + 1 < L ? m.attn_norm + (size_t)(l + 1) * H : m.final_norm;
-    CKL(launch_pdl(b_residual_norm_kernel, dim3(hsl, n), dim3(256), 0, st, bs.x, (const float*)bs.y, H,
+    CKL(pdl_launch(b_residual_norm_kernel, dim3(hsl, n), dim3(256), 0, st, bs.x, (const float*)bs.y, H,
                    ldy, zd, pstride, next_norm, xhl, lo(H), ss_next));
   }
   if (!(e = gemm_hl(m.lm_head, V, H, xhl, n, bs.logits, V, bs.err, st, 1,
                     ss + (size_t)(2 * L) * kMaxBatch, m.rms_eps)).empty()) return e;
-  CKL(launch_pdl(b_argmax_kernel, dim3((V + 4095) / 4096, n), dim3(256), 0, st, (const float*)bs.logits,
+  CKL(pdl_launch(b_argmax_kernel, dim3((V + 4095) / 4096, n), dim3(256), 0, st, (const float*)bs.logits,
                  V, best));
-  CKL(launch_pdl(b_ids_kernel, dim3(1), dim3(32), 0, st, (const unsigned long long*)best, n, bs.ids));
+  CKL(pdl_launch(b_ids_kernel, dim3(1), dim3(32), 0, st, (const unsigned long long*)best, n, bs.ids));
   const cudaError_t ce = cudaGetLastError();
   return ce == cudaSuccess ? "" : std::string("batched step launch: ") + cudaGetErrorString(ce);
 }
