@@ -409,6 +409,7 @@ class Decoder:
         trip on the decoder's stream, which waits for the caller's current
         stream first; that waits for the results."""
         import torch
+        _tensor(prompt_dev, torch.int32, "prompt_dev")
         if not 1 <= beams <= self.max_batch:
             raise ValueError("beams is 1 to max_batch")
         n, V, dev = prompt_dev.numel(), self.model.vocab, prompt_dev.device

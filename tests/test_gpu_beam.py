@@ -584,3 +584,20 @@ def test_beam_search_matches_a_search_that_replays_every_hypothesis(cuda_ok, mse
     assert dec.status() == 0 and host.status() == 0
     dec.close()
     host.close()
+
+
+def test_beam_search_refuses_other_prompts(cuda_ok):
+    """Token ids of another type, on the host or with gaps: read as int32 they
+    would be another prompt."""
+    model = synth.TINY
+    w = {k: v.cuda() for k, v in synth.make_model(model, 3).items()}
+    dec = _decoder(model, w, 64, 2, 0)
+    prompt = synth.make_prompt(12, model.vocab)
+    for bad in (prompt.cuda().long(), prompt, prompt.cuda().repeat_interleave(2)[::2]):
+        with pytest.raises(TypeError):
+            dec.beam_search(bad, 2, 3)
+    for beams, steps in ((0, 3), (3, 3), (2, 0), (2, 54)):
+        with pytest.raises(ValueError):
+            dec.beam_search(prompt.cuda(), beams, steps)
+    assert dec.status() == 0
+    dec.close()
