@@ -482,17 +482,18 @@ int mk_kv4_evict(const mk_kv4_cache* src, const mk_kv4_cache* dst, int budget, i
  * apart) gives candidates (beam, token) the score
  * cum_dev[r] + log_softmax(logits)[token]; the `beams` highest of a search,
  * compared in 64 bits, become its next beams, highest first (ties: the lowest
- * beam, then the higher logit, then the lowest token: beams with equal sums and
- * the same logits in another order tie).  The scores written may be off by 2^-18
- * and a rounding to fp32.  A call takes longer where beams' scores are closer than
- * that, as their rows are read again.  A beam with
+ * beam, then the higher logit, then the lowest token; beams with equal sums and
+ * the same logits in another order, or all raised by a constant, tie).  The
+ * scores written may be off by 2^-18 and a rounding to fp32; a call takes longer
+ * where beams are closer than that, as their rows are read again.  A beam with
  * finished_dev[r] != 0 has the one candidate (eos, cum) and its logits are not
- * read.  -inf and NaN scores are no candidates; a search with fewer
- * candidates than beams fills up with dead beams: score -inf, their own number as
- * parent, token max(eos, 0).  Writes [n_batch][beams] tokens, parents (beam numbers inside
- * the search), scores and, if asked, finished flags (the parent's, or token ==
- * eos >= 0).  finished_dev (needs eos >= 0) and finished_out_dev may be NULL;
- * outputs are arrays of their own.  vocab <= 1048576, n_batch * beams <= 65535.
+ * read.  -inf and NaN scores are no candidates; a search with fewer candidates
+ * than beams fills up with dead beams: score -inf, their own number as parent,
+ * token max(eos, 0).  Writes [n_batch][beams] tokens, parents (beam numbers
+ * inside the search), scores and, if asked, finished flags (the parent's, or
+ * token == eos >= 0).  finished_dev (needs eos >= 0) and finished_out_dev may be
+ * NULL; outputs are arrays of their own.  vocab <= 1048576, n_batch * beams <=
+ * 65535.
  * workspace_dev: mk_beam_select_workspace_bytes(...) bytes, 16-byte aligned,
  * any contents. */
 size_t mk_beam_select_workspace_bytes(int n_batch, int beams, int vocab);

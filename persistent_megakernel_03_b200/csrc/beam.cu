@@ -24,9 +24,9 @@ namespace {
 // ties make them too many, rounds over all logits find the lowest places.  A
 // second kernel, one CTA a search and one warp a beam, joins the chunks: the
 // log-sum-exp, the beam's W best (they lie in the W chunks with the highest
-// heads), then the best of W * W scores.  The chunks' sums are fp32 sums; where their
-// error could decide between candidates of two beams the join takes those beams' sums
-// again, in 64 bits and in no order, so candidates are never ordered by rounding.
+// heads), then the best of W * W scores.  The chunks' sums are fp32 sums; where
+// their error could decide between candidates of two beams the join takes those
+// beams' sums again, in 64 bits and in no order: never does that error order them.
 //
 // Bound: the logits' bytes once (4.1 MB for 8 beams of 128,256 in fp32: under
 // 1 us) beside two launches and W rounds of warp maxima in each.
@@ -252,18 +252,21 @@ __device__ __forceinline__ double key_score64(unsigned long long k) {
   return __longlong_as_double((long long)(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
 }
 
-// Largest error of a beam's log-sum-exp as the chunks give it.  Exponents in log2
-// units carry 2.3 x 2^-24 of their size (difference, product, the rounded
-// log2(e)), and the mean size under a chunk's softmax is at most the logarithm
-// of its 8,192 logits (the entropy is that mean and the sum's logarithm), 9.1 nats: 21 x 2^-24 of the
-// sum.  ex2.approx adds 4 x 2^-24 and 23 additions in a row 23 x 2^-24; the chunks are added in 64 bits.
+// Largest error of a beam's log-sum-exp as the chunks give it.  Exponents carry
+// 2.3 x 2^-24 of their size (difference, product, the rounded log2(e)), and
+// their mean size under a chunk's softmax is at most the logarithm of its 8,192
+// logits, 9.1 nats (the entropy is that mean plus the sum's logarithm): 21 x
+// 2^-24 of the sum.  ex2.approx adds 4 x 2^-24 and 23 additions in a row 23 x
+// 2^-24; the chunks are added in 64 bits.
 constexpr double kSumError = 1.0 / (1 << 18);
 
-// This thread's part of the sum of exp(logit - mx) over a row, in units of 2^-43 (x) and of 2^-86
-// (y, what those leave, of either sign): whole numbers, so that the sum does not depend on the
-// order and rows of the same logits have the same one.  At most 2^20 terms of at most
-// 2^43: modulo 2^64 they fit.  A term is rounded to either unit by an addition that leaves it in the last bits of
-// the sum; conversions to integers cost as much as the exponential.
+// This thread's part of the sum of exp(logit - mx) over a row, in units of 2^-43
+// (x) and of 2^-86 (y, what those leave, of either sign): whole numbers, so that
+// the sum does not depend on the order and rows of the same logits have the
+// same one.  At most 2^20 terms of at most 2^43: modulo 2^64 they fit.  A term is
+// rounded to either unit by an addition that leaves it in the last bits of the
+// sum (with conversions to integers and loads of single logits, 8 rows of 128,256
+// in fp32 took 1,250 us instead of 706).
 __device__ __noinline__ ulonglong2 exact_sum(const uint8_t* base, int dtype, int vocab, float mx) {
   constexpr double kOne = 0x1p9, kTwo = 1.5 * 0x1p-34;   // last bits 2^-43 and 2^-86
   ulonglong2 sum = {0ull, 0ull};
@@ -306,11 +309,11 @@ __device__ __forceinline__ bool finished_of(const SelectArgs& a, size_t row) {
 __host__ __device__ constexpr int join_threads(int beams) { return beams == 1 ? 32 : beams > 4 ? beams * 32 : 128; }
 
 // One CTA a search, one warp a beam.  HEADS: chunk heads of a lane.  WT: most beams.
-// Where candidates of two beams are closer than the error of their sums (neighbours
-// 0.1 apart are that close once in 13,000 times), those beams' sums are taken
-// again in 64 bits and the choice is made again.  It costs 0.2 to 0.8 us where nothing is
-// close (8 beams of 128,256 fp32 10.1 -> 10.5 us) and 90 to 130 us for each
-// such beam of that size; beams that all hold the same logits 706 us.
+// Where candidates of two beams are closer than the error of their sums
+// (neighbours 0.1 apart on average are that close once in 13,000 times), those
+// beams' sums are taken again in 64 bits and the choice is made again.  It costs 0.2 to
+// 0.8 us where nothing is close (8 beams of 128,256 fp32 10.1 -> 10.5 us) and
+// 90 to 130 us for each such beam of that size (8 that hold the same logits 706 us).
 template <int HEADS, int WT>
 __global__ void __launch_bounds__(join_threads(WT)) beam_join_kernel(const SelectArgs a) {
   constexpr int kOwn = WT * WT < 32 ? 1 : WT * WT / 32;   // candidates of a lane
@@ -400,7 +403,9 @@ __global__ void __launch_bounds__(join_threads(WT)) beam_join_kernel(const Selec
         sum += sum_of[i].x > -INFINITY ? (double)sum_of[i].y * exp((double)sum_of[i].x - (double)mx) : (double)sum_of[i].y;
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      const double lse = (double)mx + log(sum);
+      // log-probability: (logit - mx) - log(sum), the first difference exact, so that a constant
+      // on all logits of a row changes nothing
+      const double log_sum = log(sum);
       if (lane == 0) highest[beam] = mx;
       // the beam's W best: of the few from the bound on, again by counting
       const uint32_t least = max(bound[beam], 1u);
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(join_threads(WT)) beam_join_kernel(const Selec
           before += o.x > me.x || (o.x == me.x && o.y < me.y);
         }
         if (before < W) {
-          cand_score[beam][before] = cum + ((double)key_logit(me.x) - lse);
+          cand_score[beam][before] = cum + (((double)key_logit(me.x) - (double)mx) - log_sum);
           cand_logit[beam][before] = key_logit(me.x);
           cand_token[beam][before] = (int32_t)me.y;
         }
@@ -464,9 +469,9 @@ __global__ void __launch_bounds__(join_threads(WT)) beam_join_kernel(const Selec
           }
         }
       }
-      // Beams that a choice could have gone the other way for: of neighbours in the order, and
-      // of the last choice and each beam's next candidate.  (What is close to a choice
-      // further off is close to all in between.)
+      // Beams that a choice could have gone the other way for: of neighbours in the
+      // order, and of the last choice and each beam's next candidate.  (What is close
+      // to a choice further off is close to all in between.)
       uint32_t close = 0u;
       if (W > 1) {
         auto close_to = [&](unsigned long long key, int b, double below, int b2) -> uint32_t {
@@ -504,9 +509,10 @@ __global__ void __launch_bounds__(join_threads(WT)) beam_join_kernel(const Selec
         atomicAdd(&total[1], sum.y);
       }
       __syncthreads();
-      if (beam == b && lane < W && cand_score[b][lane] > -INFINITY)
-        cand_score[b][lane] = cum + ((double)cand_logit[b][lane] -
-                                     ((double)highest[b] + log(((double)total[0] + (double)(long long)total[1] * 0x1p-43) * 0x1p-43)));
+      if (beam == b && lane < W && cand_score[b][lane] > -INFINITY) {
+        const double all = ((double)total[0] + (double)(long long)total[1] * 0x1p-43) * 0x1p-43;
+        cand_score[b][lane] = cum + (((double)cand_logit[b][lane] - (double)highest[b]) - log(all));
+      }
       __syncthreads();
     }
   }

@@ -224,6 +224,26 @@ def test_select_orders_beams_whose_sums_differ_in_the_tail(cuda_ok):
     assert np.array_equal(par.cpu().numpy(), want[1]) and np.array_equal(tok.cpu().numpy(), want[0])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,W,V", [(8, 4, 9001), (4, 8, 70000), (3, 16, 300)])
+def test_select_rows_that_differ_by_a_constant_tie(cuda_ok, dtype, n, W, V):
+    """A constant on all logits of a row changes no log-probability: with equal sums
+    every score is a tie of all beams.  Multiples of 1/8 between -8 and 8 hold
+    the shifts, of up to 8, exactly in every type."""
+    x = (_shuffled(n, W, V, torch.float32, V).clamp(-8, 8) * 8).round() / 8
+    shift = torch.randint(-32, 33, (n * W, 1), generator=torch.Generator().manual_seed(W)).float() / 4
+    x = (x + shift).to(TYPES[dtype])
+    assert torch.equal(x.double().frac().mul(8).frac(), torch.zeros_like(x.double()))
+    tok, par, sc, _ = _run(x.cuda(), torch.full((n, W), -0.7, device="cuda"))
+    x = x.double().numpy().reshape(n, W, V)
+    for b in range(n):
+        level = x[b] - x[b].max(-1, keepdims=True)
+        order = sorted((-level[w, v], w, i, v) for w in range(W)
+                       for i, v in enumerate(np.argsort(-level[w], kind="stable")[:W]))[:W]
+        assert par[b].tolist() == [o[1] for o in order]
+        assert tok[b].tolist() == [o[3] for o in order]
+
+
 def test_select_close_beams_replayed_and_repeated(cuda_ok):
     """The same bits from a graph and from every call, also where beams are close."""
     x = _shuffled(4, 4, 20000, torch.float16, 3).cuda()
